@@ -73,6 +73,26 @@ typedef struct {
                             the workspace); ignored for the last layer, which writes y */
 } bl_layer;
 
+/* The function between the gate and the other factor of an expert (bl_moe). */
+typedef enum { BL_ACT_SILU = 0, BL_ACT_RELU2 = 1 } bl_act; /* g / (1 + exp(-g)); max(g, 0)^2 */
+
+/* A mixture-of-experts layer (bitlinear_moe_forward). Each expert's matrices are packed one
+ * after the other, each as bitlinear_quantize_weights writes it, with its own gamma. */
+typedef struct {
+  const void* router;      /* device [E][D], router_dtype BL_F32 or BL_BF16 */
+  const uint8_t* gate;     /* device [E][F][D/4] */
+  const uint8_t* up;       /* device [E][F][D/4] */
+  const uint8_t* down;     /* device [E][D][F/4] */
+  const float* gate_gamma; /* device [E] */
+  const float* up_gamma;   /* device [E] */
+  const float* down_gamma; /* device [E] */
+  int router_dtype;
+  int E, D, F;     /* experts, width of x and y, inner width of an expert */
+  int top_k;       /* experts per token */
+  int act;         /* bl_act */
+  int renormalize; /* 0: weights are the softmax over all experts; else over the chosen ones */
+} bl_moe;
+
 /* Device bytes of workspace that bitlinear_quantize_weights (for N x K) and
  * bitlinear_forward / bitlinear_contract_i32 (for M x N x K) need; the largest of the
  * three. Pure host function. Returns 0 for shapes the library rejects. */
@@ -151,6 +171,89 @@ bl_status bitlinear_act_absmax(const void* x, int x_dtype, int M, int K, float* 
 bl_status bitlinear_quantize_acts_absmax(const void* x, int x_dtype, int M, int K,
                                          const float* amax, int8_t* xq, float* scale,
                                          void* stream);
+
+/* RMS norm with the residual's addition, quantized to int8 as it is computed: the step before
+ * every BitLinear, for bitlinear_forward_quantized.
+ *   h[t,k]   = rnd(x[t,k] + residual[t,k])                (rounded to x_dtype; x if none)
+ *   rstd_t   = 1 / sqrt(mean_k h[t,k]^2 + eps)            (fp32)
+ *   p[t,k]   = fl(h[t,k] * weight[k]),  a_t = max_k |p[t,k]|
+ *   q[t,k]   = clip(rne(fl(p[t,k] * fl(127 / a_t))), -127, 127)   (0 if a_t == 0 or p == 0)
+ *   scale_t  = fl(fl(a_t * rstd_t) / 127),  normed[t,k] = rnd(fl(p[t,k] * rstd_t))
+ * The normalised row is h * rstd * weight; q * scale stands for it. rstd_t, one positive factor
+ * per row, cancels out of the codes.
+ *   x         device, [M][K], fp32 or bf16 (x_dtype).
+ *   residual  device, [M][K], x_dtype, or NULL.
+ *   weight    device, [K], fp32 or bf16 (w_dtype).
+ *   eps       1e-20 <= eps, finite (squares are summed in fp32).
+ *   h         device, [M][K], x_dtype, or NULL to skip; written only with a residual. May be x
+ *             or residual itself.
+ *   normed    device, [M][K], x_dtype, or NULL to skip: the normalised rows without the
+ *             quantization (for a router); no other argument's memory.
+ *   xq        device, [M][K] int8, written.   scale  device, [M] fp32, written.
+ *   rstd      device, [M] fp32, or NULL to skip: what bitlinear_rmsnorm_backward needs.
+ * K <= 32768, else BL_ERR_UNSUPPORTED_SHAPE. Inf/NaN in x, residual or weight, or a row whose
+ * sum of squares or largest |p| passes fp32, sets BL_ERR_NONFINITE in the status word. */
+bl_status bitlinear_rmsnorm_quantize(const void* x, const void* residual, int x_dtype,
+                                     const void* weight, int w_dtype, float eps, int M, int K,
+                                     void* h, void* normed, int8_t* xq, float* scale, float* rstd,
+                                     void* stream);
+
+/* Workspace bytes of bitlinear_rmsnorm_backward on the current device (0 for shapes it
+ * rejects). */
+size_t bitlinear_rmsnorm_backward_workspace_size(int M, int K);
+
+/* Gradient of the norm above; the quantizer passes gradients straight through, as in
+ * bitlinear_backward. With hat = h * rstd and g the gradient of the normalised rows:
+ *   grad_x[t,k]    = grad_h[t,k] + rstd_t (g w - hat mean_k(g w hat))
+ *   grad_weight[k] = sum_t g[t,k] hat[t,k]
+ * grad_x is the gradient of x and of residual alike.
+ *   grad_n       device, [M][K], fp32 or bf16 (gn_dtype): the sum of the grad_x of every layer
+ *                that read the codes.
+ *   h            device, [M][K], h_dtype: what the norm wrote (x if it had no residual).
+ *   weight       device, [K], w_dtype.   rstd  device, [M], from the norm.
+ *   grad_h       device, [M][K], gx_dtype: gradient that reaches h past the norm; or NULL.
+ *   grad_x       device, [M][K], gx_dtype, written; may be grad_h itself.
+ *   grad_weight  device, [K] fp32, written (sums in a fixed order: the same bits every time).
+ *   ws           device, bitlinear_rmsnorm_backward_workspace_size(M, K) bytes.
+ * K <= 32768, else BL_ERR_UNSUPPORTED_SHAPE. */
+bl_status bitlinear_rmsnorm_backward(const void* grad_n, int gn_dtype, const void* h, int h_dtype,
+                                     const void* weight, int w_dtype, const float* rstd,
+                                     const void* grad_h, void* grad_x, int gx_dtype,
+                                     float* grad_weight, int M, int K, void* ws, size_t ws_bytes,
+                                     void* stream);
+
+/* bitlinear_forward on activations that are int8 already (bitlinear_rmsnorm_quantize,
+ * bitlinear_quantize_acts): several layers can read one quantized batch.
+ *   y[t,n] = fl(float(sum_k c[n,k] xq[t,k]) * fl(scale_t * gamma))
+ *   xq      device, [M][K] int8 (values in [-127, 127]).   scale  device, [M] fp32.
+ *   packed, gamma, y  as in bitlinear_forward.
+ *   ws      device, at least bitlinear_workspace_size(M, N, K) bytes; may be NULL for M <= 16.
+ * Bit for bit what bitlinear_forward gives on the activations that have these codes. */
+bl_status bitlinear_forward_quantized(const int8_t* xq, const float* scale, const uint8_t* packed,
+                                      const float* gamma, void* y, int y_dtype, int M, int N, int K,
+                                      void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of bitlinear_moe_forward for M tokens (0 for a layer or M that it rejects).
+ * Pure host function. */
+size_t bitlinear_moe_workspace_size(int M, const bl_moe* layer);
+
+/* A whole mixture-of-experts layer with ternary experts, for a few tokens (decode batches):
+ *   logits[t,e] = sum_d x[t,d] router[e,d]                                        (fp32)
+ *   S_t         = the top_k experts of the largest logits (of equal ones, the lower index)
+ *   w[t,e]      = softmax(logits_t)[e], over all experts or (renormalize) over S_t
+ *   G, U        = the BitLinear outputs of x_t for gate and up of e, in fp32
+ *   i[t,e]      = act(G) * U,  o[t,e] = the BitLinear output of i[t,e] for down of e, in fp32
+ *   y_t         = sum over S_t, largest logit first, of w[t,e] o[t,e]    (fp32, rounded once)
+ * Activations are quantized per row as in bitlinear_forward; only the chosen experts' weights
+ * are read.
+ *   x      device, [M][D], fp32 or bf16.   y  device, [M][D], BL_F32 or BL_BF16.
+ *   layer  host pointer, read before the call returns.
+ *   ws     device, bitlinear_moe_workspace_size(M, layer) bytes (contents ignored).
+ * 1 <= M <= 64; E <= 512; top_k <= min(E, 16); D, F multiples of 64 with M*top_k*D, M*top_k*F
+ * and D*F below 2^31; else BL_ERR_UNSUPPORTED_SHAPE. Inf/NaN in x, or logits that are not
+ * finite, set BL_ERR_NONFINITE in the status word. */
+bl_status bitlinear_moe_forward(const void* x, int x_dtype, int M, const bl_moe* layer, void* y,
+                                int y_dtype, void* ws, size_t ws_bytes, void* stream);
 
 /* The rescale on its own: y[t,n] = fl(float(acc[t,n]) * fl(scale_t * gamma)) (fp32, or the
  * bf16 RNE of that value), for an int32 product formed elsewhere, e.g. the SUM
@@ -256,6 +359,14 @@ bl_status bitlinear_backward(const void* x, int x_dtype, const void* grad_y,
                              const uint8_t* packedT, const float* gamma, float* grad_x,
                              float* grad_w, int M, int N, int K, void* ws, size_t ws_bytes,
                              void* stream);
+
+/* bitlinear_backward for a forward that ran on int8 activations (bitlinear_forward_quantized):
+ * X~ = bf16(xq * scale) from the codes and scales themselves. Arguments, results and workspace
+ * (bitlinear_backward_workspace_size) as there; xq [M][K] and scale [M] are needed for grad_w. */
+bl_status bitlinear_backward_quantized(const int8_t* xq, const float* scale, const void* grad_y,
+                                       const uint8_t* packedT, const float* gamma, float* grad_x,
+                                       float* grad_w, int M, int N, int K, void* ws,
+                                       size_t ws_bytes, void* stream);
 
 /* The integer stage alone (test hook, same kernels as bitlinear_forward):
  * acc[t,n] = sum_k c[n,k] * xq[t,k].

@@ -28,7 +28,9 @@ EXPORTS = (
     "bitlinear_quantize_acts_absmax", "bitlinear_rescale", "bitlinear_chain_workspace_size",
     "bitlinear_chain_forward", "bitlinear_base3_row_bytes", "bitlinear_pack_base3",
     "bitlinear_forward_base3", "bitlinear_pack_transpose", "bitlinear_backward_workspace_size",
-    "bitlinear_backward",
+    "bitlinear_backward", "bitlinear_backward_quantized", "bitlinear_forward_quantized",
+    "bitlinear_rmsnorm_quantize", "bitlinear_rmsnorm_backward_workspace_size",
+    "bitlinear_rmsnorm_backward", "bitlinear_moe_workspace_size", "bitlinear_moe_forward",
     "bitlinear_forward", "bitlinear_forward_noalloc", "bitlinear_contract_i32",
     "bitlinear_get_device_status",
     "bitlinear_debug_timeout_probe", "bitlinear_debug_plan", "bitlinear_status_string",
@@ -39,6 +41,13 @@ class Layer(ctypes.Structure):
     """bl_layer of include/bitlinear.h: one layer of a chain."""
     _fields_ = [("packed", ctypes.c_void_p), ("gamma", ctypes.c_void_p), ("N", ctypes.c_int),
                 ("K", ctypes.c_int), ("src", ctypes.c_int), ("out", ctypes.c_void_p)]
+
+
+class Moe(ctypes.Structure):
+    """bl_moe of include/bitlinear.h: a mixture-of-experts layer."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("router", "gate", "up", "down", "gate_gamma",
+                                               "up_gamma", "down_gamma")] + [
+        (n, ctypes.c_int) for n in ("router_dtype", "E", "D", "F", "top_k", "act", "renormalize")]
 
 
 class BitLinearError(RuntimeError):
@@ -94,6 +103,20 @@ def load_library() -> ctypes.CDLL:
     lib.bitlinear_backward_workspace_size.restype = sz
     lib.bitlinear_backward.argtypes = [p, i, p, p, p, p, p, i, i, i, p, sz, p]
     lib.bitlinear_backward.restype = i
+    lib.bitlinear_backward_quantized.argtypes = [p, p, p, p, p, p, p, i, i, i, p, sz, p]
+    lib.bitlinear_backward_quantized.restype = i
+    lib.bitlinear_forward_quantized.argtypes = [p, p, p, p, p, i, i, i, i, p, sz, p]
+    lib.bitlinear_forward_quantized.restype = i
+    lib.bitlinear_rmsnorm_quantize.argtypes = [p, p, i, p, i, f, i, i, p, p, p, p, p, p]
+    lib.bitlinear_rmsnorm_quantize.restype = i
+    lib.bitlinear_rmsnorm_backward_workspace_size.argtypes = [i, i]
+    lib.bitlinear_rmsnorm_backward_workspace_size.restype = sz
+    lib.bitlinear_rmsnorm_backward.argtypes = [p, i, p, i, p, i, p, p, p, i, p, i, i, p, sz, p]
+    lib.bitlinear_rmsnorm_backward.restype = i
+    lib.bitlinear_moe_workspace_size.argtypes = [i, ctypes.POINTER(Moe)]
+    lib.bitlinear_moe_workspace_size.restype = sz
+    lib.bitlinear_moe_forward.argtypes = [p, i, i, ctypes.POINTER(Moe), p, i, p, sz, p]
+    lib.bitlinear_moe_forward.restype = i
     lib.bitlinear_forward.argtypes = [p, i, p, p, p, i, i, i, i, p, sz, p]
     lib.bitlinear_forward.restype = i
     lib.bitlinear_forward_noalloc.argtypes = [p, i, p, p, p, i, i, i, i, p]
@@ -136,6 +159,34 @@ def _dtype_code(t: torch.Tensor) -> int:
 def _stream(stream) -> int:
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
+
+
+def _run(fn, what: str, device: torch.device, stream, *args) -> None:
+    """Calls fn(*args, stream) with `device` current (on its current stream if none is given)."""
+    at = device.index
+    if at == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), what)
+        return
+    with torch.cuda.device(at):
+        _check(fn(*args, _stream(stream)), what)
+
+
+def _take(t: torch.Tensor, name: str, shape, dtype, device: torch.device) -> int:
+    """Address of a contiguous tensor of this shape and type (one of them) on this device."""
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype not in dtype if isinstance(dtype, tuple) else t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    return _dev(t, name)
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _take_or_none(t, name, shape, dtype, device):
+    return None if t is None else _take(t, name, shape, dtype, device)
 
 
 def workspace_size(M: int, N: int, K: int) -> int:
@@ -361,6 +412,192 @@ def backward(x: torch.Tensor, grad_y: torch.Tensor, packedT: torch.Tensor, gamma
         _dev(ws, "ws") if ws is not None else None, ws.numel() if ws is not None else 0,
         _stream(stream)), "bitlinear_backward")
     return gx, gw
+
+
+def backward_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
+    """A caller-owned device workspace for backward and backward_quantized."""
+    n = int(load_library().bitlinear_backward_workspace_size(M, N, K))
+    if n == 0:
+        raise BitLinearError(2, "bitlinear_backward_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def backward_quantized(xq: torch.Tensor, scale: torch.Tensor, grad_y: torch.Tensor,
+                       packedT: torch.Tensor, gamma: torch.Tensor, need_x: bool = True,
+                       need_w: bool = True, ws: torch.Tensor | None = None, stream=None):
+    """backward for a forward that ran on int8 activations xq [M][K] with scales [M]."""
+    lib = load_library()
+    (M, K), N, dev = xq.shape, grad_y.shape[1], xq.device
+    gx = torch.empty((M, K), dtype=torch.float32, device=dev) if need_x else None
+    gw = torch.empty((N, K), dtype=torch.float32, device=dev) if need_w else None
+    if ws is None and need_w:
+        ws = backward_workspace(M, N, K, dev)
+    _run(lib.bitlinear_backward_quantized, "bitlinear_backward_quantized", dev, stream,
+         _take(xq, "xq", (M, K), torch.int8, dev), _take(scale, "scale", (M,), torch.float32, dev),
+         _take(grad_y, "grad_y", (M, N), torch.bfloat16, dev),
+         _take(packedT, "packedT", (K, N // 4), torch.uint8, dev),
+         _take(gamma, "gamma", (1,), torch.float32, dev),
+         gx.data_ptr() if need_x else None, gw.data_ptr() if need_w else None, M, N, K,
+         None if ws is None else _take(ws, "ws", ws.shape, torch.uint8, dev),
+         0 if ws is None else ws.numel())
+    return gx, gw
+
+
+def forward_quantized(xq: torch.Tensor, scale: torch.Tensor, packed: torch.Tensor,
+                      gamma: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
+                      y: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """BitLinear forward of int8 activations xq [M][K] with scales [M] (rmsnorm_quantize,
+    quantize_acts): y [M][N]."""
+    lib = load_library()
+    (M, K), N, dev = xq.shape, packed.shape[0], xq.device
+    if y is None:
+        y = torch.empty((M, N), dtype=out_dtype, device=dev)
+    if ws is None and M > FEW_TOKENS:
+        ws = workspace(M, N, K, dev)
+    _run(lib.bitlinear_forward_quantized, "bitlinear_forward_quantized", dev, stream,
+         _take(xq, "xq", (M, K), torch.int8, dev), _take(scale, "scale", (M,), torch.float32, dev),
+         _take(packed, "packed", (N, K // 4), torch.uint8, dev),
+         _take(gamma, "gamma", (1,), torch.float32, dev), _take(y, "y", (M, N), _FLOATS, dev),
+         _dtype_code(y), M, N, K, None if ws is None else _take(ws, "ws", ws.shape, torch.uint8, dev),
+         0 if ws is None else ws.numel())
+    return y
+
+
+FEW_TOKENS = 16  # forward_quantized needs no workspace up to here
+
+
+def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                     eps: float = 1e-5, h: torch.Tensor | None = None,
+                     xq: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                     rstd: torch.Tensor | None = None, normed: torch.Tensor | None = None,
+                     stream=None):
+    """RMS norm of h = x + residual with gain weight [K], as int8 codes: (xq [M][K], scale [M],
+    h [M][K], rstd [M]). h is x itself without a residual; it may be given as x or residual
+    (added in place). normed, if given, receives the normalised rows themselves."""
+    lib = load_library()
+    (M, K), dev, dt = x.shape, x.device, x.dtype
+    if residual is None:
+        h = x
+    elif h is None:
+        h = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if xq is None:
+        xq = torch.empty((M, K), dtype=torch.int8, device=dev)
+    if scale is None:
+        scale = torch.empty(M, dtype=torch.float32, device=dev)
+    if rstd is None:
+        rstd = torch.empty(M, dtype=torch.float32, device=dev)
+    _run(lib.bitlinear_rmsnorm_quantize, "bitlinear_rmsnorm_quantize", dev, stream,
+         _dev(x, "x"), _take_or_none(residual, "residual", (M, K), dt, dev), _dtype_code(x),
+         _take(weight, "weight", (K,), _FLOATS, dev), _dtype_code(weight), float(eps), M, K,
+         None if residual is None else _take(h, "h", (M, K), dt, dev),
+         _take_or_none(normed, "normed", (M, K), dt, dev), _take(xq, "xq", (M, K), torch.int8, dev),
+         _take(scale, "scale", (M,), torch.float32, dev), _take(rstd, "rstd", (M,), torch.float32, dev))
+    return xq, scale, h, rstd
+
+
+def rmsnorm_backward_workspace(M: int, K: int, device="cuda") -> torch.Tensor:
+    """A caller-owned device workspace for rmsnorm_backward."""
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        n = int(load_library().bitlinear_rmsnorm_backward_workspace_size(M, K))
+    if n == 0:
+        raise BitLinearError(2, "bitlinear_rmsnorm_backward_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def rmsnorm_backward(grad_n: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                     rstd: torch.Tensor, grad_h: torch.Tensor | None = None,
+                     out_dtype: torch.dtype = torch.float32, grad_x: torch.Tensor | None = None,
+                     grad_weight: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                     stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gradient of rmsnorm_quantize (straight through the quantizer): (grad_x [M][K], for x and
+    the residual alike, grad_weight fp32 [K]) from the gradient grad_n of the normalised rows
+    and, if given, the gradient grad_h that reaches h past the norm (of grad_x's type; grad_x
+    may be grad_h itself)."""
+    lib = load_library()
+    (M, K), dev = h.shape, h.device
+    if grad_x is None:
+        grad_x = torch.empty((M, K), dtype=out_dtype, device=dev)
+    if grad_weight is None:
+        grad_weight = torch.empty(K, dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = rmsnorm_backward_workspace(M, K, dev)
+    _run(lib.bitlinear_rmsnorm_backward, "bitlinear_rmsnorm_backward", dev, stream,
+         _take(grad_n, "grad_n", (M, K), _FLOATS, dev), _dtype_code(grad_n), _dev(h, "h"),
+         _dtype_code(h), _take(weight, "weight", (K,), _FLOATS, dev), _dtype_code(weight),
+         _take(rstd, "rstd", (M,), torch.float32, dev),
+         _take_or_none(grad_h, "grad_h", (M, K), grad_x.dtype, dev),
+         _take(grad_x, "grad_x", (M, K), _FLOATS, dev), _dtype_code(grad_x),
+         _take(grad_weight, "grad_weight", (K,), torch.float32, dev), M, K,
+         _take(ws, "ws", ws.shape, torch.uint8, dev), ws.numel())
+    return grad_x, grad_weight
+
+
+ACTIVATIONS = {"silu": 0, "relu2": 1}
+
+
+def quantize_expert_weights(W: torch.Tensor, eps: float = 1e-5,
+                            stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """quantize_weights of every expert of W [E][N][K] -> (packed [E][N][K/4], gamma [E])."""
+    E, N, K = W.shape
+    packed = torch.empty((E, N, K // 4), dtype=torch.uint8, device=W.device)
+    one = torch.empty((E, 4), dtype=torch.float32, device=W.device)  # each gamma 16-byte aligned
+    ws = workspace(1, N, K, W.device)
+    with torch.cuda.device(W.device), torch.cuda.stream(stream):
+        for e in range(E):
+            quantize_weights(W[e], eps, packed[e], one[e, :1], ws, stream)
+        return packed, one[:, 0].contiguous()
+
+
+class MoeLayer:
+    """The weights of a mixture-of-experts layer for moe_forward: router [E][D] (fp32 or bf16)
+    and the packed experts gate, up [E][F][D/4] and down [E][D][F/4] with their gammas [E]
+    (quantize_expert_weights). Keeps the tensors alive."""
+
+    def __init__(self, router: torch.Tensor, gate: torch.Tensor, gate_gamma: torch.Tensor,
+                 up: torch.Tensor, up_gamma: torch.Tensor, down: torch.Tensor,
+                 down_gamma: torch.Tensor, top_k: int, activation: str = "silu",
+                 renormalize: bool = True):
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {tuple(ACTIVATIONS)}")
+        (E, D), F, dev = router.shape, gate.shape[1], router.device
+        self.E, self.D, self.F, self.top_k, self.device = E, D, F, int(top_k), dev
+        self.tensors = (router, gate, up, down, gate_gamma, up_gamma, down_gamma)
+        self.struct = Moe(
+            _take(router, "router", (E, D), _FLOATS, dev),
+            _take(gate, "gate", (E, F, D // 4), torch.uint8, dev),
+            _take(up, "up", (E, F, D // 4), torch.uint8, dev),
+            _take(down, "down", (E, D, F // 4), torch.uint8, dev),
+            _take(gate_gamma, "gate_gamma", (E,), torch.float32, dev),
+            _take(up_gamma, "up_gamma", (E,), torch.float32, dev),
+            _take(down_gamma, "down_gamma", (E,), torch.float32, dev),
+            _dtype_code(router), E, D, F, int(top_k), ACTIVATIONS[activation], int(bool(renormalize)))
+
+
+def moe_workspace(M: int, layer: MoeLayer) -> torch.Tensor:
+    """A caller-owned device workspace for moe_forward of up to 64 tokens."""
+    n = int(load_library().bitlinear_moe_workspace_size(M, ctypes.byref(layer.struct)))
+    if n == 0:
+        raise BitLinearError(2, "bitlinear_moe_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=layer.device)
+
+
+def moe_forward(x: torch.Tensor, layer: MoeLayer, out_dtype: torch.dtype = torch.bfloat16,
+                y: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """A mixture-of-experts layer for a few tokens (up to 64): x [M][D] -> y [M][D]."""
+    lib = load_library()
+    M, dev = x.shape[0], layer.device
+    if y is None:
+        y = torch.empty((M, layer.D), dtype=out_dtype, device=dev)
+    if ws is None:
+        ws = moe_workspace(M, layer)
+    _run(lib.bitlinear_moe_forward, "bitlinear_moe_forward", dev, stream,
+         _take(x, "x", (M, layer.D), _FLOATS, dev), _dtype_code(x), M, ctypes.byref(layer.struct),
+         _take(y, "y", (M, layer.D), _FLOATS, dev), _dtype_code(y),
+         _take(ws, "ws", ws.shape, torch.uint8, dev), ws.numel())
+    return y
 
 
 def forward(x: torch.Tensor, packed: torch.Tensor, gamma: torch.Tensor,

@@ -15,13 +15,16 @@
 #include "../../include/bitlinear.h"
 #include "act_quant.cuh"
 #include "common.cuh"
+#include "few_tokens.cuh"
 #include "gemm_bf16.cuh"
 #include "gemm_prefill.cuh"
 #include "gemm_skinny.cuh"
 #include "gemv.cuh"
 #include "gemv3.cuh"
+#include "moe.cuh"
 #include "per_device.h"
 #include "rescale.cuh"
+#include "rmsnorm.cuh"
 #include "weight_quant.cuh"
 
 namespace {
@@ -34,6 +37,7 @@ static_assert(kSkinnyMaxM <= bl::sk::MAX_M, "the skinny kernel stages per-token 
 constexpr int kGemvMaxSmem = 200 * 1024;  // xq rows held in shared memory by the GEMV
 constexpr unsigned long long kWaitLimitNs = 4000000000ull;  // 4 s per mbarrier wait
 constexpr int kMinKbPerSplit = 8;  // skinny split-K: K blocks per split, at least
+constexpr float kNormMinEps = 1e-20f;  // the norm's squares are fp32: smaller ones would vanish below a smaller eps
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -861,6 +865,19 @@ int grid_for(long long work, int per_block) {
       1, std::min<long long>((work + per_block - 1) / per_block, 16ll * num_sms())));
 }
 
+// grad_w = G^T X~ from the int8 codes and scales: both operands transposed into the
+// workspace, then the contraction over the tokens.
+bl_status launch_grad_w(const int8_t* xq, const float* scale, const void* grad_y, float* grad_w,
+                        int M, int N, int K, const BwdWs& w, cudaStream_t s) {
+  const int tiles_g = ((w.Mp + 63) / 64) * (N / 64);
+  bl::transpose_bf16_kernel<0><<<grid_for(tiles_g, 1), 256, 0, s>>>(grad_y, nullptr, w.gT, M, N,
+                                                                     w.Mp);
+  const int tiles_x = ((w.Mp + 63) / 64) * (K / 64);
+  bl::transpose_bf16_kernel<1><<<grid_for(tiles_x, 1), 256, 0, s>>>(xq, scale, w.xT, M, K, w.Mp);
+  if (launch_status() != BL_OK) return BL_ERR_CUDA;
+  return launch_gemm_bf16<false>(w.gT, w.xT, nullptr, grad_w, N, K, w.Mp, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -900,14 +917,29 @@ bl_status bitlinear_backward(const void* x, int x_dtype, const void* grad_y,
     if (ws_bytes < w.bytes) return BL_ERR_WORKSPACE;
     bl_status st = launch_act_quant(x, x_dtype, M, K, w.f.xq, w.f.scale, nullptr, s);
     if (st != BL_OK) return st;
-    const int tiles_g = ((w.Mp + 63) / 64) * (N / 64);
-    bl::transpose_bf16_kernel<0><<<grid_for(tiles_g, 1), 256, 0, s>>>(grad_y, nullptr, w.gT, M,
-                                                                       N, w.Mp);
-    const int tiles_x = ((w.Mp + 63) / 64) * (K / 64);
-    bl::transpose_bf16_kernel<1><<<grid_for(tiles_x, 1), 256, 0, s>>>(w.f.xq, w.f.scale, w.xT,
-                                                                       M, K, w.Mp);
-    if (launch_status() != BL_OK) return BL_ERR_CUDA;
-    st = launch_gemm_bf16<false>(w.gT, w.xT, nullptr, grad_w, N, K, w.Mp, s);
+    st = launch_grad_w(w.f.xq, w.f.scale, grad_y, grad_w, M, N, K, w, s);
+    if (st != BL_OK) return st;
+  }
+  if (grad_x) return launch_gemm_bf16<true>(grad_y, packedT, gamma, grad_x, M, K, N, s);
+  return BL_OK;
+}
+
+bl_status bitlinear_backward_quantized(const int8_t* xq, const float* scale, const void* grad_y,
+                                       const uint8_t* packedT, const float* gamma, float* grad_x,
+                                       float* grad_w, int M, int N, int K, void* ws,
+                                       size_t ws_bytes, void* stream) {
+  if (!grad_y || (!grad_x && !grad_w)) return BL_ERR_INVALID_ARG;
+  if (grad_x && (!packedT || !gamma)) return BL_ERR_INVALID_ARG;
+  if (grad_w && (!xq || !scale || !ws)) return BL_ERR_INVALID_ARG;
+  if (!shape_ok(M, N, K) || N % 64 != 0) return BL_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(grad_y) || !aligned16(xq) || !aligned16(scale) || !aligned16(packedT) ||
+      !aligned16(gamma) || !aligned16(grad_x) || !aligned16(grad_w) || !aligned16(ws))
+    return BL_ERR_MISALIGNED;  // a null pointer is aligned
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (grad_w) {
+    const BwdWs w = bwd_ws_layout(ws, M, N, K);
+    if (ws_bytes < w.bytes) return BL_ERR_WORKSPACE;
+    const bl_status st = launch_grad_w(xq, scale, grad_y, grad_w, M, N, K, w, s);
     if (st != BL_OK) return st;
   }
   if (grad_x) return launch_gemm_bf16<true>(grad_y, packedT, gamma, grad_x, M, K, N, s);
@@ -1088,6 +1120,250 @@ bl_status bitlinear_contract_i32(const int8_t* xq, const uint8_t* packed, int32_
   if (M <= kSkinnyMaxM)
     return launch_skinny(xq, packed, w.rowsum, nullptr, nullptr, acc, BL_I32, M, N, K, ws, s);
   return launch_gemm(xq, packed, w.rowsum, nullptr, nullptr, acc, BL_I32, M, N, K, s);
+}
+
+}  // extern "C"
+
+namespace {
+
+// ------------------------------------------------------------------ layer on int8 codes
+constexpr int kFewMaxM = 16;  // M above this runs the forward's tensor-core kernels
+
+template <int NT>
+bl_status launch_few(const int8_t* xq, const float* scale, const uint8_t* packed,
+                     const float* gamma, void* y, int y_dtype, int M, int N, int K,
+                     cudaStream_t s) {
+  constexpr int kRows = bl::kFewThreads / 32 * 16;
+  const int grid = (N + kRows - 1) / kRows;
+  if (y_dtype == BL_BF16)
+    bl::few_tokens_kernel<NT, true><<<grid, bl::kFewThreads, 0, s>>>(xq, scale, packed, gamma, y, M, N, K);
+  else
+    bl::few_tokens_kernel<NT, false><<<grid, bl::kFewThreads, 0, s>>>(xq, scale, packed, gamma, y, M, N, K);
+  return launch_status();
+}
+
+// ------------------------------------------------------------------ norm
+// Threads per row and vectors of 8 elements per thread.
+struct NormPlan {
+  int threads, V;
+};
+NormPlan norm_plan(int K) {
+  const int nv = K / 8;
+  NormPlan p{};
+  p.V = nv <= 512 ? 1 : nv <= 1024 ? 2 : 4;
+  p.threads = ((nv + p.V - 1) / p.V + 31) / 32 * 32;
+  return p;
+}
+
+bool norm_shape_ok(int M, int K) { return shape_ok(M, 1, K) && K <= bl::kNormMaxK; }
+
+template <bool kBf16>
+bl_status launch_rmsnorm(const void* x, const void* r, const void* w, int w_bf16, float eps, int M,
+                         int K, void* h, void* normed, int8_t* xq, float* scale, float* rstd,
+                         cudaStream_t s) {
+  const NormPlan p = norm_plan(K);
+  switch (p.V) {
+    case 1:
+      bl::rmsnorm_quant_kernel<kBf16, 1><<<M, p.threads, 0, s>>>(x, r, w, w_bf16, eps, K, h, normed, xq, scale, rstd);
+      break;
+    case 2:
+      bl::rmsnorm_quant_kernel<kBf16, 2><<<M, p.threads, 0, s>>>(x, r, w, w_bf16, eps, K, h, normed, xq, scale, rstd);
+      break;
+    default:
+      bl::rmsnorm_quant_kernel<kBf16, 4><<<M, p.threads, 0, s>>>(x, r, w, w_bf16, eps, K, h, normed, xq, scale, rstd);
+  }
+  return launch_status();
+}
+
+// Blocks of the gradient kernel (each leaves one row of partial sums of grad_w).
+int norm_backward_blocks(int M) { return std::min(M, 2 * num_sms()); }
+
+struct NormBwdArgs {
+  const void *g, *h, *w;
+  int w_bf16;
+  const float* rstd;
+  const void* grad_h;
+  void* grad_x;
+  float *grad_w, *part;
+  int M, K;
+};
+
+template <bool H, bool G, bool O, int V, bool R>
+bl_status launch_norm_backward_t(const NormBwdArgs& a, int threads, cudaStream_t s) {
+  const int blocks = norm_backward_blocks(a.M);
+  bl::rmsnorm_backward_kernel<H, G, O, V, R><<<blocks, threads, 0, s>>>(
+      a.g, a.h, a.w, a.w_bf16, a.rstd, a.grad_h, a.grad_x, a.part, a.M, a.K);
+  if (launch_status() != BL_OK) return BL_ERR_CUDA;
+  bl::rmsnorm_grad_weight_kernel<<<a.K / 32, bl::kNormGwThreads, 0, s>>>(a.part, blocks, a.K, a.grad_w);
+  return launch_status();
+}
+
+template <bool H, bool G, bool O>
+bl_status launch_norm_backward_v(const NormBwdArgs& a, cudaStream_t s) {
+  const NormPlan p = norm_plan(a.K);
+  if (p.V == 1) return launch_norm_backward_t<H, G, O, 1, false>(a, p.threads, s);
+  if (p.V == 2) return launch_norm_backward_t<H, G, O, 2, false>(a, p.threads, s);
+  if (p.threads <= bl::kNormMaxThreads / 2) return launch_norm_backward_t<H, G, O, 4, false>(a, p.threads, s);
+  return launch_norm_backward_t<H, G, O, 4, true>(a, p.threads, s);
+}
+
+template <bool H>
+bl_status launch_norm_backward_h(const NormBwdArgs& a, bool g_bf16, bool o_bf16, cudaStream_t s) {
+  if (g_bf16) return o_bf16 ? launch_norm_backward_v<H, true, true>(a, s) : launch_norm_backward_v<H, true, false>(a, s);
+  return o_bf16 ? launch_norm_backward_v<H, false, true>(a, s) : launch_norm_backward_v<H, false, false>(a, s);
+}
+
+bool float_dtype(int d) { return d == BL_F32 || d == BL_BF16; }
+
+// ------------------------------------------------------------------ mixture of experts
+bl_status moe_check(int M, const bl_moe* m) {
+  if (!m || !m->router || !m->gate || !m->up || !m->down || !m->gate_gamma || !m->up_gamma ||
+      !m->down_gamma || !float_dtype(m->router_dtype))
+    return BL_ERR_INVALID_ARG;
+  if (m->act != BL_ACT_SILU && m->act != BL_ACT_RELU2) return BL_ERR_INVALID_ARG;
+  if (M < 1 || M > bl::kMoeMaxTokens || m->E < 1 || m->E > bl::kMoeMaxExperts || m->top_k < 1 ||
+      m->top_k > bl::kMoeMaxTopK || m->top_k > m->E || m->D % 64 != 0 || m->F % 64 != 0 ||
+      m->F < 64 || !shape_ok(M * m->top_k, m->F, m->D) || !shape_ok(M * m->top_k, m->D, m->F))
+    return BL_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(m->router) || !aligned16(m->gate) || !aligned16(m->up) || !aligned16(m->down) ||
+      !aligned16(m->gate_gamma) || !aligned16(m->up_gamma) || !aligned16(m->down_gamma))
+    return BL_ERR_MISALIGNED;
+  return BL_OK;
+}
+
+// Workspace of bitlinear_moe_forward.
+struct MoeWs {
+  FwdWs x, h;       // codes, scales and row sums of the tokens and of the inner rows
+  int* ids;         // [M * top_k]
+  float* weights;   // [M * top_k]
+  float* inner;     // [M * top_k][F]
+  float* part;      // [M * top_k][D]
+  size_t bytes;
+};
+MoeWs moe_ws_layout(void* base, int M, const bl_moe& m) {
+  MoeWs w{};
+  const int P = M * m.top_k;
+  char* p = static_cast<char*>(base);
+  w.x = fwd_ws_layout(p, M, m.D);
+  p += w.x.bytes;
+  w.h = fwd_ws_layout(p, P, m.F);
+  p += w.h.bytes;
+  auto take = [&p](size_t bytes) { char* q = p; p += align_up(bytes, 256); return q; };
+  w.ids = reinterpret_cast<int*>(take(static_cast<size_t>(P) * 4));
+  w.weights = reinterpret_cast<float*>(take(static_cast<size_t>(P) * 4));
+  w.inner = reinterpret_cast<float*>(take(static_cast<size_t>(P) * m.F * 4));
+  w.part = reinterpret_cast<float*>(take(static_cast<size_t>(P) * m.D * 4));
+  w.bytes = static_cast<size_t>(p - static_cast<char*>(base));
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+bl_status bitlinear_forward_quantized(const int8_t* xq, const float* scale, const uint8_t* packed,
+                                      const float* gamma, void* y, int y_dtype, int M, int N, int K,
+                                      void* ws, size_t ws_bytes, void* stream) {
+  if (!xq || !scale || !packed || !gamma || !y) return BL_ERR_INVALID_ARG;
+  if (!float_dtype(y_dtype)) return BL_ERR_INVALID_ARG;
+  if (!shape_ok(M, N, K)) return BL_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(xq) || !aligned16(scale) || !aligned16(packed) || !aligned16(gamma) || !aligned16(y))
+    return BL_ERR_MISALIGNED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M <= 8) return launch_few<1>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
+  if (M <= kFewMaxM) return launch_few<2>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
+  if (!ws) return BL_ERR_WORKSPACE;
+  if (!aligned16(ws)) return BL_ERR_MISALIGNED;
+  if (ws_bytes < fwd_ws_bytes(M, N, K)) return BL_ERR_WORKSPACE;
+  FwdWs w = fwd_ws_layout(ws, M, K);
+  uint4* zero = nullptr;
+  long long zero_n16 = 0;
+  if (M <= kSkinnyMaxM) skinny_zero_region(ws, M, N, K, &zero, &zero_n16);
+  bl::rowsum_i8_kernel<<<M, bl::kAqThreads, 0, s>>>(xq, K, w.rowsum, zero, zero_n16);
+  if (launch_status() != BL_OK) return BL_ERR_CUDA;
+  if (M <= kSkinnyMaxM)
+    return launch_skinny(xq, packed, w.rowsum, scale, gamma, y, y_dtype, M, N, K, ws, s);
+  return launch_gemm(xq, packed, w.rowsum, scale, gamma, y, y_dtype, M, N, K, s);
+}
+
+bl_status bitlinear_rmsnorm_quantize(const void* x, const void* residual, int x_dtype,
+                                     const void* weight, int w_dtype, float eps, int M, int K,
+                                     void* h, void* normed, int8_t* xq, float* scale, float* rstd,
+                                     void* stream) {
+  if (!x || !weight || !xq || !scale) return BL_ERR_INVALID_ARG;
+  if (!float_dtype(x_dtype) || !float_dtype(w_dtype)) return BL_ERR_INVALID_ARG;
+  if (!(eps >= kNormMinEps) || !std::isfinite(eps)) return BL_ERR_INVALID_ARG;
+  if (!norm_shape_ok(M, K)) return BL_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(h) ||
+      !aligned16(normed) || !aligned16(xq) || !aligned16(scale) || !aligned16(rstd))
+    return BL_ERR_MISALIGNED;  // a null pointer is aligned
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int wb = w_dtype == BL_BF16 ? 1 : 0;
+  return x_dtype == BL_BF16
+             ? launch_rmsnorm<true>(x, residual, weight, wb, eps, M, K, h, normed, xq, scale, rstd, s)
+             : launch_rmsnorm<false>(x, residual, weight, wb, eps, M, K, h, normed, xq, scale, rstd, s);
+}
+
+size_t bitlinear_rmsnorm_backward_workspace_size(int M, int K) {
+  if (!norm_shape_ok(M, K)) return 0;
+  return align_up(static_cast<size_t>(norm_backward_blocks(M)) * K * 4, 256);
+}
+
+bl_status bitlinear_rmsnorm_backward(const void* grad_n, int gn_dtype, const void* h, int h_dtype,
+                                     const void* weight, int w_dtype, const float* rstd,
+                                     const void* grad_h, void* grad_x, int gx_dtype,
+                                     float* grad_weight, int M, int K, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  if (!grad_n || !h || !weight || !rstd || !grad_x || !grad_weight) return BL_ERR_INVALID_ARG;
+  if (!float_dtype(gn_dtype) || !float_dtype(h_dtype) || !float_dtype(w_dtype) || !float_dtype(gx_dtype))
+    return BL_ERR_INVALID_ARG;
+  if (!norm_shape_ok(M, K)) return BL_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(grad_n) || !aligned16(h) || !aligned16(weight) || !aligned16(rstd) ||
+      !aligned16(grad_h) || !aligned16(grad_x) || !aligned16(grad_weight) || !aligned16(ws))
+    return BL_ERR_MISALIGNED;
+  if (!ws || ws_bytes < bitlinear_rmsnorm_backward_workspace_size(M, K)) return BL_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const NormBwdArgs a{grad_n, h, weight, w_dtype == BL_BF16 ? 1 : 0, rstd, grad_h, grad_x, grad_weight,
+                      static_cast<float*>(ws), M, K};
+  return h_dtype == BL_BF16 ? launch_norm_backward_h<true>(a, gn_dtype == BL_BF16, gx_dtype == BL_BF16, s)
+                            : launch_norm_backward_h<false>(a, gn_dtype == BL_BF16, gx_dtype == BL_BF16, s);
+}
+
+size_t bitlinear_moe_workspace_size(int M, const bl_moe* layer) {
+  if (moe_check(M, layer) != BL_OK) return 0;
+  return align_up(moe_ws_layout(nullptr, M, *layer).bytes, 256);
+}
+
+bl_status bitlinear_moe_forward(const void* x, int x_dtype, int M, const bl_moe* layer, void* y,
+                                int y_dtype, void* ws, size_t ws_bytes, void* stream) {
+  if (!x || !y || !float_dtype(x_dtype) || !float_dtype(y_dtype)) return BL_ERR_INVALID_ARG;
+  bl_status st = moe_check(M, layer);
+  if (st != BL_OK) return st;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(ws)) return BL_ERR_MISALIGNED;
+  const bl_moe& m = *layer;
+  if (!ws || ws_bytes < moe_ws_layout(nullptr, M, m).bytes) return BL_ERR_WORKSPACE;
+  const MoeWs w = moe_ws_layout(ws, M, m);
+  const int P = M * m.top_k, rb = m.router_dtype == BL_BF16 ? 1 : 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (x_dtype == BL_BF16)
+    bl::moe_route_kernel<true><<<M, 256, 0, s>>>(x, m.router, rb, m.D, m.E, m.top_k, m.renormalize, w.ids, w.weights);
+  else
+    bl::moe_route_kernel<false><<<M, 256, 0, s>>>(x, m.router, rb, m.D, m.E, m.top_k, m.renormalize, w.ids, w.weights);
+  st = launch_act_quant(x, x_dtype, M, m.D, w.x.xq, w.x.scale, w.x.rowsum, s);
+  if (st != BL_OK) return st;
+  constexpr int kRows = bl::kMoeThreads / 32 * 16;
+  bl::moe_gate_up_kernel<<<dim3((m.F + kRows - 1) / kRows, m.E), bl::kMoeThreads, 0, s>>>(
+      w.ids, w.x.xq, w.x.scale, w.x.rowsum, m.gate, m.up, m.gate_gamma, m.up_gamma, P, m.top_k, m.D, m.F,
+      m.act, w.inner);
+  st = launch_act_quant(w.inner, BL_F32, P, m.F, w.h.xq, w.h.scale, w.h.rowsum, s);
+  if (st != BL_OK) return st;
+  bl::moe_down_kernel<<<dim3((m.D + kRows - 1) / kRows, m.E), bl::kMoeThreads, 0, s>>>(
+      w.ids, w.h.xq, w.h.scale, w.h.rowsum, m.down, m.down_gamma, P, m.D, m.F, w.part);
+  if (y_dtype == BL_BF16)
+    bl::moe_combine_kernel<true><<<dim3((m.D + 255) / 256, M), 256, 0, s>>>(w.part, w.weights, m.D, m.top_k, y);
+  else
+    bl::moe_combine_kernel<false><<<dim3((m.D + 255) / 256, M), 256, 0, s>>>(w.part, w.weights, m.D, m.top_k, y);
+  return launch_status();
 }
 
 size_t bitlinear_base3_row_bytes(int K) {
