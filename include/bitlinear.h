@@ -227,7 +227,8 @@ bl_status bitlinear_rmsnorm_backward(const void* grad_n, int gn_dtype, const voi
  *   y[t,n] = fl(float(sum_k c[n,k] xq[t,k]) * fl(scale_t * gamma))
  *   xq      device, [M][K] int8 (values in [-127, 127]).   scale  device, [M] fp32.
  *   packed, gamma, y  as in bitlinear_forward.
- *   ws      device, at least bitlinear_workspace_size(M, N, K) bytes; may be NULL for M <= 16.
+ *   ws      device, at least bitlinear_workspace_size(M, N, K) bytes; may be NULL for
+ *           M <= 8 with K <= 65536 and M <= 16 with K <= 32768, which need none.
  * Bit for bit what bitlinear_forward gives on the activations that have these codes. */
 bl_status bitlinear_forward_quantized(const int8_t* xq, const float* scale, const uint8_t* packed,
                                       const float* gamma, void* y, int y_dtype, int M, int N, int K,

@@ -453,7 +453,7 @@ def forward_quantized(xq: torch.Tensor, scale: torch.Tensor, packed: torch.Tenso
     (M, K), N, dev = xq.shape, packed.shape[0], xq.device
     if y is None:
         y = torch.empty((M, N), dtype=out_dtype, device=dev)
-    if ws is None and M > FEW_TOKENS:
+    if ws is None and (M > FEW_TOKENS or K > 32768):
         ws = workspace(M, N, K, dev)
     _run(lib.bitlinear_forward_quantized, "bitlinear_forward_quantized", dev, stream,
          _take(xq, "xq", (M, K), torch.int8, dev), _take(scale, "scale", (M,), torch.float32, dev),
@@ -464,7 +464,7 @@ def forward_quantized(xq: torch.Tensor, scale: torch.Tensor, packed: torch.Tenso
     return y
 
 
-FEW_TOKENS = 16  # forward_quantized needs no workspace up to here
+FEW_TOKENS = 16  # forward_quantized needs no workspace up to here (with K <= 32768)
 
 
 def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,

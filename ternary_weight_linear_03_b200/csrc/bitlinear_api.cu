@@ -1129,17 +1129,82 @@ namespace {
 // ------------------------------------------------------------------ layer on int8 codes
 constexpr int kFewMaxM = 16;  // M above this runs the forward's tensor-core kernels
 
-template <int NT>
+// Whether a call runs the few-token kernel: a cluster's warps hold every code in registers.
+bool use_few(int M, int K) {
+  return M <= kFewMaxM &&
+         K <= 256 * bl::few_steps(M <= 8 ? 1 : 2) * bl::kFewMaxWarps * bl::kFewMaxCluster;
+}
+
+// Clusters of the few-token kernel that the current device holds at once: a second wave would
+// wait for the first.
+template <int NT, bool kPairs, bool kOBf16>
+int few_clusters(int cs, int warps) {
+  static bl::PerDevice resident[bl::kFewMaxCluster + 1][bl::kFewMaxWarps + 1];
+  return resident[cs][warps].get(current_device(), [&](int) {
+    int n = 0;
+    auto kern = bl::few_tokens_kernel<NT, kPairs, kOBf16>;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(cs);
+    c.blockDim = dim3(32 * warps);
+    c.dynamicSmemBytes = warps * bl::few_depth(NT) * 1024;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             bl::kFewMaxWarps * bl::few_depth(NT) * 1024) != cudaSuccess)
+      return 0;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeClusterDimension;
+    a[0].val.clusterDim.x = cs;
+    a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+    c.attrs = a;
+    c.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(&n, kern, &c) == cudaSuccess ? n : 0;
+  });
+}
+
+template <int NT, bool kPairs, bool kOBf16>
+bl_status launch_few_t(const int8_t* xq, const float* scale, const uint8_t* packed,
+                       const float* gamma, void* y, int M, int N, int K, cudaStream_t s) {
+  // the fewest blocks whose warps cover K
+  constexpr int kPerWarp = 256 * bl::few_steps(NT);
+  const int along = (K + kPerWarp - 1) / kPerWarp;
+  int cs = 1;
+  while ((along + cs - 1) / cs > bl::kFewMaxWarps) cs *= 2;
+  const int warps = (along + cs - 1) / cs;
+  const int most = few_clusters<NT, kPairs, kOBf16>(cs, warps);
+  if (most < 1) return BL_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(std::min((N + 15) / 16, most) * cs);
+  cfg.blockDim = dim3(32 * warps);
+  cfg.dynamicSmemBytes = warps * bl::few_depth(NT) * 1024;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cs;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cs > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, bl::few_tokens_kernel<NT, kPairs, kOBf16>, xq, scale, packed, gamma,
+                         y, M, N, K, cs) != cudaSuccess)
+    return BL_ERR_CUDA;
+  return launch_status();
+}
+
+template <int NT, bool kPairs>
+bl_status launch_few_n(const int8_t* xq, const float* scale, const uint8_t* packed,
+                       const float* gamma, void* y, int y_dtype, int M, int N, int K,
+                       cudaStream_t s) {
+  return y_dtype == BL_BF16
+             ? launch_few_t<NT, kPairs, true>(xq, scale, packed, gamma, y, M, N, K, s)
+             : launch_few_t<NT, kPairs, false>(xq, scale, packed, gamma, y, M, N, K, s);
+}
+
 bl_status launch_few(const int8_t* xq, const float* scale, const uint8_t* packed,
                      const float* gamma, void* y, int y_dtype, int M, int N, int K,
                      cudaStream_t s) {
-  constexpr int kRows = bl::kFewThreads / 32 * 16;
-  const int grid = (N + kRows - 1) / kRows;
-  if (y_dtype == BL_BF16)
-    bl::few_tokens_kernel<NT, true><<<grid, bl::kFewThreads, 0, s>>>(xq, scale, packed, gamma, y, M, N, K);
-  else
-    bl::few_tokens_kernel<NT, false><<<grid, bl::kFewThreads, 0, s>>>(xq, scale, packed, gamma, y, M, N, K);
-  return launch_status();
+  if (M > 8) return launch_few_n<2, false>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
+  if (M > 4) return launch_few_n<1, false>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
+  return launch_few_n<1, true>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
 }
 
 // ------------------------------------------------------------------ norm
@@ -1270,8 +1335,7 @@ bl_status bitlinear_forward_quantized(const int8_t* xq, const float* scale, cons
   if (!aligned16(xq) || !aligned16(scale) || !aligned16(packed) || !aligned16(gamma) || !aligned16(y))
     return BL_ERR_MISALIGNED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (M <= 8) return launch_few<1>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
-  if (M <= kFewMaxM) return launch_few<2>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
+  if (use_few(M, K)) return launch_few(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
   if (!ws) return BL_ERR_WORKSPACE;
   if (!aligned16(ws)) return BL_ERR_MISALIGNED;
   if (ws_bytes < fwd_ws_bytes(M, N, K)) return BL_ERR_WORKSPACE;

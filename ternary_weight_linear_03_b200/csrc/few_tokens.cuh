@@ -29,83 +29,257 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
 }
 
 // 256 trits of 16 rows: wa, wb the lane's 16 bytes of rows g and g + 8, q[n][i] the 16 codes of
-// token 8 n + g that belong to word i of them. acc[n]: rows g (0, 1) and g + 8 (2, 3), tokens
-// 8 n + 2 t and 8 n + 2 t + 1.
-template <int NT>
-__device__ __forceinline__ void ternary_step(int (&acc)[NT][4], const uint4& wa, const uint4& wb,
+// column 8 n + g that belong to word i of them. acc[j][n]: rows g (0, 1) and g + 8 (2, 3), columns
+// 8 n + 2 t and 8 n + 2 t + 1 of the products with fragment j. The masks are what bounds this
+// (the logic pipe takes a warp's instruction in two cycles), so the planes stay where they
+// are in the word and an accumulator per plane takes the factor 4^j.
+//   kPairs = false: fragment j is plane j, (w & 3 4^j); a column is a token. 4 masks a word.
+//   kPairs = true, for up to 4 tokens, which leave half of the 8 columns empty: fragment j is
+//     planes 0 .. j, w & (4^(j+1) - 1), so the last is the word itself and needs no mask. With
+//     P_j the products of fragment j, plane j is (P_j - P_(j-1)) / 4^j: an even column holds the
+//     token's codes of plane j, the odd one behind it those of plane j + 1, to be subtracted.
+//     3 masks a word (70B up, one token: 15.2 -> 13.8 us with both steps).
+template <int NT, bool kPairs>
+__device__ __forceinline__ void ternary_step(int (&acc)[4][NT][4], const uint4& wa, const uint4& wb,
                                              const uint4 (&q)[NT][4]) {
 #pragma unroll
   for (int i = 0; i < 4; i += 2)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t a0 = (word_of(wa, i) >> (2 * j)) & 0x03030303u;
-      const uint32_t a1 = (word_of(wb, i) >> (2 * j)) & 0x03030303u;
-      const uint32_t a2 = (word_of(wa, i + 1) >> (2 * j)) & 0x03030303u;
-      const uint32_t a3 = (word_of(wb, i + 1) >> (2 * j)) & 0x03030303u;
+      const uint32_t m = kPairs ? (j == 3 ? 0xffffffffu : ((4u << (2 * j)) - 1u) * 0x01010101u)
+                                : 0x03030303u << (2 * j);
+      const uint32_t a0 = word_of(wa, i) & m, a1 = word_of(wb, i) & m;
+      const uint32_t a2 = word_of(wa, i + 1) & m, a3 = word_of(wb, i + 1) & m;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        mma_u8s8(acc[n], a0, a1, a2, a3, word_of(q[n][i], j), word_of(q[n][i + 1], j));
+        mma_u8s8(acc[j][n], a0, a1, a2, a3, word_of(q[n][i], j), word_of(q[n][i + 1], j));
     }
 }
+// The exact sum: of column e & 1 (kPairs = false), or of the token of both columns (e even).
+template <int NT, bool kPairs>
+__device__ __forceinline__ int ternary_sum(const int (&acc)[4][NT][4], int n, int e) {
+  if (kPairs)
+    return acc[0][n][e] + ((acc[1][n][e] - acc[0][n][e + 1]) >> 2) +
+           ((acc[2][n][e] - acc[1][n][e + 1]) >> 4) + ((acc[3][n][e] - acc[2][n][e + 1]) >> 6);
+  return acc[0][n][e] + (acc[1][n][e] >> 2) + (acc[2][n][e] >> 4) + (acc[3][n][e] >> 6);
+}
+// Codes of an odd column (kPairs): those of the plane behind, none behind the last.
+__device__ __forceinline__ uint4 next_plane(const uint4& v) { return make_uint4(v.y, v.z, v.w, 0u); }
 
-constexpr int kFewThreads = 128;
+constexpr int kFewMaxWarps = 8;     // warps of a block
+constexpr int kFewMaxCluster = 8;
+constexpr int kFewRound = 32;       // tiles of 16 rows between two joins of the sums
+// 256-trit steps of 16 rows (1 KB) that a warp keeps in flight: two blocks of 8 warps and their
+// sums fill the shared memory of an SM.
+__host__ __device__ constexpr int few_depth(int NT) { return NT == 1 ? 12 : 8; }
+// Steps of a warp: as many as its registers hold codes for (fewer steps per warp mean more
+// sums to join for the same weights: one token, 70B up, 1 / 2 / 4 steps: 17.8 / 15.8 / 13.9 us).
+__host__ __device__ constexpr int few_steps(int NT) { return NT == 1 ? 4 : 2; }
 
-// y[t,n] = fl(float(acc) fl(scale_t gamma)) for M <= 8 NT tokens: a warp per 16 rows of the
-// packed weights, token codes straight from global memory.
-template <int NT, bool kOBf16>
-__global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most `kPending` of this thread's groups are in flight.
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// The 16 bytes at shared address `addr` of this block, in block `rank` of the cluster.
+__device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  int4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+// One stage of transpose4: the lanes that differ in bit `mask` exchange b of the one without
+// the bit for a of the one with it.
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b, bool has, int mask) {
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, has ? a : b, mask);
+  a = has ? got : a;
+  b = has ? b : got;
+}
+__device__ __forceinline__ void exchange(uint4& a, uint4& b, bool has, int mask) {
+  exchange(a.x, b.x, has, mask);
+  exchange(a.y, b.y, has, mask);
+  exchange(a.z, b.z, has, mask);
+  exchange(a.w, b.w, has, mask);
+}
+// v[i] of lane t and v[t] of lane i change places within each four lanes (t = lane % 4).
+__device__ __forceinline__ void transpose4(uint4 (&v)[4], int t) {
+  exchange(v[0], v[2], t & 2, 2);
+  exchange(v[1], v[3], t & 2, 2);
+  exchange(v[0], v[1], t & 1, 1);
+  exchange(v[2], v[3], t & 1, 1);
+}
+
+// y[t,n] = fl(float(sum_k c q) fl(scale_t gamma)) for M <= 8 NT tokens (4 with kPairs). Bound by the packed
+// weights' bytes. K is split over all warps of a cluster of blocks, few_steps steps of 256 to one,
+// so that a warp can keep its part of every token in registers for the whole kernel: the
+// codes are read once per cluster, not once per block (they are the same lines for
+// everybody, and L2 hands out one line at a time), and the loop has no shared-memory reads.
+// Each warp then streams its columns of the cluster's row tiles through a ring of its own in
+// shared memory (a lane reads back what it copied itself, so nobody else is waited for), and
+// adds a tile's integer sums to the block's (exact in any order): no warp waits for another
+// before the join. The ring holds what the memory delivers while the codes arrive. The stream has no bounds to check: rows past N and
+// chunks past K read the last ones, and meet outputs that are not written and codes that
+// are zero.
+template <int NT, bool kPairs, bool kOBf16>
+__global__ void __launch_bounds__(32 * kFewMaxWarps, 2) few_tokens_kernel(
     const int8_t* __restrict__ xq, const float* __restrict__ scale, const uint8_t* __restrict__ packed,
-    const float* __restrict__ gamma_ptr, void* __restrict__ y, int M, int N, int K) {
-  __shared__ int rowsum[8 * NT];
+    const float* __restrict__ gamma_ptr, void* __restrict__ y, int M, int N, int K, int cs) {
+  constexpr int S = few_steps(NT);
+  constexpr int kAhead = few_depth(NT) / S;  // tiles whose weights are in flight
+  extern __shared__ __align__(16) uint8_t ring_all[];  // [warp][tile][step][row half][lane] 16 bytes
+  __shared__ __align__(16) int sums[kFewRound * 16 * 8 * NT];  // [row of the round][token]
+  __shared__ float factor[8 * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  for (int t = warp; t < M; t += kFewThreads / 32) {
-    const uint4* row = reinterpret_cast<const uint4*>(xq + static_cast<size_t>(t) * K);
-    int s = 0;
-    for (int c = lane; c < K / 16; c += 32) {
-      const uint4 v = row[c];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s = __dp4a(static_cast<int>(word_of(v, i)), 0x01010101, s);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) rowsum[t] = s;
-  }
-  __syncthreads();
-  const int row0 = (blockIdx.x * (kFewThreads / 32) + warp) * 16;
-  if (row0 >= N) return;
+  const int warps = blockDim.x >> 5;
+  const uint32_t rank = cs > 1 ? cluster_rank() : 0u;
   const int chunks = K / 64;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  const int ra = row0 + g, rb = row0 + g + 8;
-  const uint4* pa = reinterpret_cast<const uint4*>(packed + static_cast<size_t>(ra) * (K / 4));
-  const uint4* pb = reinterpret_cast<const uint4*>(packed + static_cast<size_t>(rb) * (K / 4));
-  int acc[NT][4] = {};
-  for (int c = t4; c - t4 < chunks; c += 4) {
-    const bool in = c < chunks;
-    const uint4 wa = (in && ra < N) ? ld_stream_v4(pa + c) : zero;
-    const uint4 wb = (in && rb < N) ? ld_stream_v4(pb + c) : zero;
-    uint4 q[NT][4];
+  const int c = 4 * S * (static_cast<int>(rank) * warps + warp) + t4;  // this lane's chunks: c, c + 4, ...
+  // 16-row tiles first, first + clusters, ...: `count` of them
+  const int tiles = (N + 15) / 16, clusters = gridDim.x / cs, first = blockIdx.x / cs;
+  const int count = (tiles - first + clusters - 1) / clusters;
+  const size_t pitch = static_cast<size_t>(K / 4);
+  const uint32_t ring = smem_u32(ring_all) + warp * kAhead * S * 1024 + lane * 16;
+  auto fetch = [&](uint32_t slot, int i) {
+    if (i < count) {
+      const int row = (first + i * clusters) * 16 + g;
+      const uint8_t* a = packed + min(row, N - 1) * pitch;
+      const uint8_t* b = packed + min(row + 8, N - 1) * pitch;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int t = 8 * n + g;
-      const uint4* px = reinterpret_cast<const uint4*>(xq + static_cast<size_t>(t) * K);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[n][i] = (in && t < M) ? px[4 * c + i] : zero;
-    }
-    ternary_step<NT>(acc, wa, wb, q);
-  }
-  const float gamma = *gamma_ptr;
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int t = 8 * n + 2 * t4 + (e & 1), r = (e < 2) ? ra : rb;
-      if (t < M && r < N) {
-        const float v = __fmul_rn(__int2float_rn(acc[n][e] - rowsum[t]), __fmul_rn(scale[t], gamma));
-        const size_t at = static_cast<size_t>(t) * N + r;
-        if (kOBf16) static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
-        else static_cast<float*>(y)[at] = v;
+      for (int s = 0; s < S; ++s) {
+        const int at = 16 * min(c + 4 * s, chunks - 1);
+        cp_async16(slot + s * 1024, a + at);
+        cp_async16(slot + s * 1024 + 512, b + at);
       }
     }
+    cp_async_commit();
+  };
+  for (int i = threadIdx.x; i < kFewRound * 32 * NT; i += blockDim.x)
+    reinterpret_cast<uint4*>(sums)[i] = make_uint4(0u, 0u, 0u, 0u);
+  // the kernel before may have written the weights too: nothing is read ahead of this wait
+  grid_dependency_wait();
+#pragma unroll
+  for (int r = 0; r < kAhead; ++r) fetch(ring + r * S * 1024, r);
+  uint4 q[S][NT][4];
+  int minus[NT][2];  // -sum of the warp's codes of the tokens of this lane's columns
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int t = kPairs ? g >> 1 : 8 * n + g;
+    const uint4* row = reinterpret_cast<const uint4*>(xq + static_cast<size_t>(min(t, M - 1)) * K);
+    int sum = 0;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      // Lane t needs the four 16-byte units of chunk c + 4 s. With more than 8 tokens the lanes
+      // of a row read neighbouring units (a request then touches 8 lines, not 16) and exchange
+      // them (16 tokens, 70B up / down: 22.9 / 27.9 -> 20.7 / 23.6 us; 8 tokens, up: 14.9 -> 15.6).
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int chunk = NT == 1 ? c + 4 * s : c - t4 + 4 * s + i, unit = NT == 1 ? i : t4;
+        v[i] = (t < M && chunk < chunks) ? row[4 * chunk + unit] : make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (NT > 1) transpose4(v, t4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum = __dp4a(static_cast<int>(word_of(v[i], j)), 0x01010101, sum);
+        q[s][n][i] = kPairs && (g & 1) ? next_plane(v[i]) : v[i];
+      }
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    minus[n][0] = -__shfl_sync(0xffffffffu, sum, 8 * t4);
+    minus[n][1] = kPairs ? 0 : -__shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
+  }
+  if (threadIdx.x < M) factor[threadIdx.x] = __fmul_rn(scale[threadIdx.x], *gamma_ptr);
+  __syncthreads();  // the sums are zero
+  uint32_t slot = ring;
+  for (int i0 = 0; i0 < count; i0 += kFewRound) {
+    const int i1 = min(count, i0 + kFewRound);
+    for (int i = i0; i < i1; ++i) {
+      int acc[4][NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[0][n][e] = minus[n][e & 1];
+          acc[1][n][e] = acc[2][n][e] = acc[3][n][e] = 0;
+        }
+      cp_async_wait<kAhead - 1>();
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        const uint4 wa = ld_shared_v4(slot + s * 1024), wb = ld_shared_v4(slot + s * 1024 + 512);
+        ternary_step<NT, kPairs>(acc, wa, wb, q[s]);
+      }
+      fetch(slot, i + kAhead);
+      slot = slot + S * 1024 == ring + kAhead * S * 1024 ? ring : slot + S * 1024;
+      int* to = sums + ((i - i0) * 16 + g) * 8 * NT;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; e += kPairs ? 2 : 1) {
+          const int t = kPairs ? t4 : 8 * n + 2 * t4 + (e & 1);
+          if (t < M) atomicAdd(to + (e < 2 ? 0 : 64 * NT) + t, ternary_sum<NT, kPairs>(acc, n, e));
+        }
+    }
+    if (cs > 1) cluster_barrier(); else __syncthreads();
+    // The cluster's blocks share the tiles of the round; a thread takes four tokens of a row.
+    const int share = (i1 - i0 - static_cast<int>(rank) + cs - 1) / cs, quads = (M + 3) / 4;
+    for (int u = threadIdx.x; u < share * quads * 16; u += blockDim.x) {
+      const int r = u & 15, at = (u >> 4) / quads, t0 = 4 * ((u >> 4) - at * quads);
+      const int i = i0 + static_cast<int>(rank) + at * cs, row = (first + i * clusters) * 16 + r;
+      const int* from = sums + ((i - i0) * 16 + r) * 8 * NT + t0;
+      int sum[4] = {};
+      if (cs > 1) {
+#pragma unroll 4
+        for (int k = 0; k < cs; ++k) {
+          const int4 v = ld_cluster_v4(smem_u32(from), k);
+          sum[0] += v.x; sum[1] += v.y; sum[2] += v.z; sum[3] += v.w;
+        }
+      } else {
+        const int4 v = *reinterpret_cast<const int4*>(from);
+        sum[0] = v.x; sum[1] = v.y; sum[2] = v.z; sum[3] = v.w;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = t0 + e;
+        if (t < M && row < N) {
+          const float v = __fmul_rn(__int2float_rn(sum[e]), factor[t]);
+          const size_t to = static_cast<size_t>(t) * N + row;
+          if (kOBf16) static_cast<__nv_bfloat16*>(y)[to] = __float2bfloat16_rn(v);
+          else static_cast<float*>(y)[to] = v;
+        }
+      }
+    }
+    if (cs > 1) cluster_barrier(); else __syncthreads();  // nobody reads these sums any more
+    if (i1 < count) {
+      for (int i = threadIdx.x; i < kFewRound * 32 * NT; i += blockDim.x)
+        reinterpret_cast<uint4*>(sums)[i] = make_uint4(0u, 0u, 0u, 0u);
+      __syncthreads();
+    }
+  }
 }
 
 }  // namespace bl

@@ -125,7 +125,7 @@ __device__ __forceinline__ int moe_pairs_of(const int* __restrict__ ids, int pai
 
 // One 16-row tile of `rows` against up to 8 pairs of codes (pair list[i0 + g] reads row
 // list[...] / div of q).
-__device__ __forceinline__ void moe_tile(int (&acc)[1][4], const uint8_t* __restrict__ w, int row0,
+__device__ __forceinline__ void moe_tile(int (&acc)[4][1][4], const uint8_t* __restrict__ w, int row0,
                                          int K, const int8_t* __restrict__ q, const int8_t* qrow) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3, chunks = K / 64;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -138,7 +138,7 @@ __device__ __forceinline__ void moe_tile(int (&acc)[1][4], const uint8_t* __rest
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       v[0][i] = (in && qrow) ? reinterpret_cast<const uint4*>(qrow)[4 * c + i] : zero;
-    ternary_step<1>(acc, wa, wb, v);
+    ternary_step<1, false>(acc, wa, wb, v);
   }
 }
 
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kMoeThreads) moe_gate_up_kernel(
   const float gg = gate_gamma[e], gu = up_gamma[e];
   for (int i0 = 0; i0 < n; i0 += 8) {
     const int8_t* qrow = i0 + g < n ? xq + static_cast<size_t>(list[i0 + g] / top_k) * D : nullptr;
-    int ag[1][4] = {}, au[1][4] = {};
+    int ag[4][1][4] = {}, au[4][1][4] = {};
     moe_tile(ag, gate + e * per, row0, D, xq, qrow);
     moe_tile(au, up + e * per, row0, D, xq, qrow);
 #pragma unroll
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kMoeThreads) moe_gate_up_kernel(
       if (i < n) {
         const int p = list[i], t = p / top_k;
         const float s = xscale[t];
-        const float G = __fmul_rn(__int2float_rn(ag[0][j] - xsum[t]), __fmul_rn(s, gg));
-        const float U = __fmul_rn(__int2float_rn(au[0][j] - xsum[t]), __fmul_rn(s, gu));
+        const float G = __fmul_rn(__int2float_rn(ternary_sum<1, false>(ag, 0, j) - xsum[t]), __fmul_rn(s, gg));
+        const float U = __fmul_rn(__int2float_rn(ternary_sum<1, false>(au, 0, j) - xsum[t]), __fmul_rn(s, gu));
         inner[static_cast<size_t>(p) * F + row0 + g + (j < 2 ? 0 : 8)] = __fmul_rn(moe_act(G, act), U);
       }
     }
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kMoeThreads) moe_down_kernel(
   const float gd = down_gamma[e];
   for (int i0 = 0; i0 < n; i0 += 8) {
     const int8_t* qrow = i0 + g < n ? hq + static_cast<size_t>(list[i0 + g]) * F : nullptr;
-    int acc[1][4] = {};
+    int acc[4][1][4] = {};
     moe_tile(acc, down + e * (static_cast<size_t>(D) * (F / 4)), row0, F, hq, qrow);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kMoeThreads) moe_down_kernel(
       if (i < n) {
         const int p = list[i];
         part[static_cast<size_t>(p) * D + row0 + g + (j < 2 ? 0 : 8)] =
-            __fmul_rn(__int2float_rn(acc[0][j] - hsum[p]), __fmul_rn(hscale[p], gd));
+            __fmul_rn(__int2float_rn(ternary_sum<1, false>(acc, 0, j) - hsum[p]), __fmul_rn(hscale[p], gd));
       }
     }
   }

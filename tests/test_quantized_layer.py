@@ -46,7 +46,7 @@ def _codes(M, K, seed):
 
 SHAPES = [(M, N, K) for M in (1, 2, 7, 8, 9, 16, 17, 40) for N, K in ((37, 64), (300, 192), (640, 1536))] + [
     (1, 1, 64), (3, 129, 320), (5, 8640, 3200), (16, 3200, 8640), (12, 1000, 28672), (15, 64, 28672),
-    (257, 200, 448), (4, 70, 65536)]
+    (257, 200, 448), (4, 70, 65536), (16, 70, 65536)]
 
 
 @pytest.mark.gpu
@@ -72,6 +72,23 @@ def test_forward_equals_forward_of_the_unquantized(M):
     x = syn.activations(M, 1536, seed=M, outlier_frac=0.01).cuda()
     packed, gamma = bl.quantize_weights(syn.weights(640, 1536, 0.02, seed=1).cuda())
     assert torch.equal(bl.forward(x, packed, gamma), bl.forward_quantized(*bl.quantize_acts(x), packed, gamma))
+
+
+@pytest.mark.gpu
+def test_forward_of_very_many_rows():
+    """More rows than the GPU's blocks join at once (several rounds of 32 tiles of 16 per block),
+    the last tile ragged; the reference is the exact fp32 product of the codes (below 2^24)."""
+    M, N, K = 3, 160001, 8192
+    q, s = _codes(M, K, 4)
+    q, s = q.cuda(), s.cuda()
+    g = torch.Generator(device="cuda").manual_seed(5)
+    u = torch.randint(0, 3, (4, N, K // 16, 4), generator=g, device="cuda", dtype=torch.uint8)
+    packed = (u[0] | u[1] << 2 | u[2] << 4 | u[3] << 6).view(N, K // 4)
+    gamma = torch.full((1,), 0.5, device="cuda")
+    y = bl.forward_quantized(q, s, packed, gamma, out_dtype=torch.float32)
+    for a in range(0, N, 20000):
+        c = u[:, a:a + 20000].permute(1, 2, 0, 3).reshape(-1, K).float() - 1
+        assert torch.equal(y[:, a:a + 20000], (q.float() @ c.T) * (s * gamma)[:, None])
 
 
 @pytest.mark.gpu
