@@ -1137,12 +1137,12 @@ bool use_few(int M, int K) {
 
 // Clusters of the few-token kernel that the current device holds at once: a second wave would
 // wait for the first.
-template <int NT, bool kPairs, bool kOBf16>
+template <int NT, int MODE, bool kOBf16>
 int few_clusters(int cs, int warps) {
   static bl::PerDevice resident[bl::kFewMaxCluster + 1][bl::kFewMaxWarps + 1];
   return resident[cs][warps].get(current_device(), [&](int) {
     int n = 0;
-    auto kern = bl::few_tokens_kernel<NT, kPairs, kOBf16>;
+    auto kern = bl::few_tokens_kernel<NT, MODE, kOBf16>;
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3(cs);
     c.blockDim = dim3(32 * warps);
@@ -1160,7 +1160,7 @@ int few_clusters(int cs, int warps) {
   });
 }
 
-template <int NT, bool kPairs, bool kOBf16>
+template <int NT, int MODE, bool kOBf16>
 bl_status launch_few_t(const int8_t* xq, const float* scale, const uint8_t* packed,
                        const float* gamma, void* y, int M, int N, int K, cudaStream_t s) {
   // the fewest blocks whose warps cover K
@@ -1169,7 +1169,7 @@ bl_status launch_few_t(const int8_t* xq, const float* scale, const uint8_t* pack
   int cs = 1;
   while ((along + cs - 1) / cs > bl::kFewMaxWarps) cs *= 2;
   const int warps = (along + cs - 1) / cs;
-  const int most = few_clusters<NT, kPairs, kOBf16>(cs, warps);
+  const int most = few_clusters<NT, MODE, kOBf16>(cs, warps);
   if (most < 1) return BL_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(std::min((N + 15) / 16, most) * cs);
@@ -1184,27 +1184,27 @@ bl_status launch_few_t(const int8_t* xq, const float* scale, const uint8_t* pack
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cs > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, bl::few_tokens_kernel<NT, kPairs, kOBf16>, xq, scale, packed, gamma,
+  if (cudaLaunchKernelEx(&cfg, bl::few_tokens_kernel<NT, MODE, kOBf16>, xq, scale, packed, gamma,
                          y, M, N, K, cs) != cudaSuccess)
     return BL_ERR_CUDA;
   return launch_status();
 }
 
-template <int NT, bool kPairs>
+template <int NT, int MODE>
 bl_status launch_few_n(const int8_t* xq, const float* scale, const uint8_t* packed,
                        const float* gamma, void* y, int y_dtype, int M, int N, int K,
                        cudaStream_t s) {
   return y_dtype == BL_BF16
-             ? launch_few_t<NT, kPairs, true>(xq, scale, packed, gamma, y, M, N, K, s)
-             : launch_few_t<NT, kPairs, false>(xq, scale, packed, gamma, y, M, N, K, s);
+             ? launch_few_t<NT, MODE, true>(xq, scale, packed, gamma, y, M, N, K, s)
+             : launch_few_t<NT, MODE, false>(xq, scale, packed, gamma, y, M, N, K, s);
 }
 
 bl_status launch_few(const int8_t* xq, const float* scale, const uint8_t* packed,
                      const float* gamma, void* y, int y_dtype, int M, int N, int K,
                      cudaStream_t s) {
-  if (M > 8) return launch_few_n<2, false>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
-  if (M > 4) return launch_few_n<1, false>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
-  return launch_few_n<1, true>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
+  if (M > 8) return launch_few_n<2, bl::kFour>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
+  if (M > 4) return launch_few_n<1, bl::kFour>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
+  return launch_few_n<1, bl::kPairs>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
 }
 
 // ------------------------------------------------------------------ norm
@@ -1298,28 +1298,62 @@ bl_status moe_check(int M, const bl_moe* m) {
 
 // Workspace of bitlinear_moe_forward.
 struct MoeWs {
-  FwdWs x, h;       // codes, scales and row sums of the tokens and of the inner rows
+  int8_t* xq;       // [M][D]
+  float* scale;     // [M]
+  float* logits;    // [M][E]
   int* ids;         // [M * top_k]
   float* weights;   // [M * top_k]
   float* inner;     // [M * top_k][F]
   float* part;      // [M * top_k][D]
+  int8_t* hq;       // [M * top_k][F]
+  float* hscale;    // [M * top_k]
+  unsigned* amax;   // [M * top_k], cleared by every call
   size_t bytes;
 };
 MoeWs moe_ws_layout(void* base, int M, const bl_moe& m) {
   MoeWs w{};
-  const int P = M * m.top_k;
+  const size_t P = static_cast<size_t>(M) * m.top_k;
   char* p = static_cast<char*>(base);
-  w.x = fwd_ws_layout(p, M, m.D);
-  p += w.x.bytes;
-  w.h = fwd_ws_layout(p, P, m.F);
-  p += w.h.bytes;
   auto take = [&p](size_t bytes) { char* q = p; p += align_up(bytes, 256); return q; };
-  w.ids = reinterpret_cast<int*>(take(static_cast<size_t>(P) * 4));
-  w.weights = reinterpret_cast<float*>(take(static_cast<size_t>(P) * 4));
-  w.inner = reinterpret_cast<float*>(take(static_cast<size_t>(P) * m.F * 4));
-  w.part = reinterpret_cast<float*>(take(static_cast<size_t>(P) * m.D * 4));
+  w.xq = reinterpret_cast<int8_t*>(take(static_cast<size_t>(M) * m.D));
+  w.scale = reinterpret_cast<float*>(take(M * 4));
+  w.logits = reinterpret_cast<float*>(take(static_cast<size_t>(M) * m.E * 4));
+  w.ids = reinterpret_cast<int*>(take(P * 4));
+  w.weights = reinterpret_cast<float*>(take(P * 4));
+  w.inner = reinterpret_cast<float*>(take(P * m.F * 4));
+  w.part = reinterpret_cast<float*>(take(P * m.D * 4));
+  w.hq = reinterpret_cast<int8_t*>(take(P * m.F));
+  w.hscale = reinterpret_cast<float*>(take(P * 4));
+  w.amax = reinterpret_cast<unsigned*>(take(P * 4));
   w.bytes = static_cast<size_t>(p - static_cast<char*>(base));
   return w;
+}
+
+template <int NT, int MODE, bool kDown>
+bl_status launch_moe_expert(bl::MoeArgs a, cudaStream_t s) {
+  auto kern = bl::moe_expert_kernel<NT, MODE, kDown>;
+  constexpr int kSmem = bl::kMoeWarps * bl::kMoeRingBytes + bl::kMoeSumBytes;
+  static bl::PerDevice configured;
+  if (!set_smem_limit_once(configured, kern, kSmem)) return BL_ERR_CUDA;
+  const int per_warp = 256 * bl::few_steps(NT), K = kDown ? a.F : a.D;
+  const int along = (K + per_warp - 1) / per_warp;
+  for (a.wk = 1; a.wk < along && a.wk < bl::kMoeWarps; a.wk *= 2) {
+  }
+  a.passes = (along + a.wk - 1) / a.wk;
+  // no more blocks than tiles of the experts that can have a token
+  const long long tiles = static_cast<long long>(std::min(a.E, a.M * a.top_k)) * ((kDown ? a.D : a.F) / 16);
+  const int grid = static_cast<int>(std::min<long long>(tiles, 2ll * num_sms()));
+  return launch_ex(kern, dim3(grid), dim3(bl::kMoeThreads), kSmem, s, true, a);
+}
+
+// The gate and up products, the codes of what comes out, the down products.
+template <int NT, int MODE>
+bl_status launch_moe(const bl::MoeArgs& a, const MoeWs& w, cudaStream_t s) {
+  bl_status st = launch_moe_expert<NT, MODE, false>(a, s);
+  if (st != BL_OK) return st;
+  st = launch_act_quant_chain(w.inner, BL_F32, a.M * a.top_k, a.F, w.hq, w.hscale, nullptr, s,
+                              reinterpret_cast<const float*>(w.amax));
+  return st != BL_OK ? st : launch_moe_expert<NT, MODE, true>(a, s);
 }
 
 }  // namespace
@@ -1407,27 +1441,51 @@ bl_status bitlinear_moe_forward(const void* x, int x_dtype, int M, const bl_moe*
   const bl_moe& m = *layer;
   if (!ws || ws_bytes < moe_ws_layout(nullptr, M, m).bytes) return BL_ERR_WORKSPACE;
   const MoeWs w = moe_ws_layout(ws, M, m);
-  const int P = M * m.top_k, rb = m.router_dtype == BL_BF16 ? 1 : 0;
+  const int rb = m.router_dtype == BL_BF16 ? 1 : 0, n_clear = M * m.top_k;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (x_dtype == BL_BF16)
-    bl::moe_route_kernel<true><<<M, 256, 0, s>>>(x, m.router, rb, m.D, m.E, m.top_k, m.renormalize, w.ids, w.weights);
-  else
-    bl::moe_route_kernel<false><<<M, 256, 0, s>>>(x, m.router, rb, m.D, m.E, m.top_k, m.renormalize, w.ids, w.weights);
-  st = launch_act_quant(x, x_dtype, M, m.D, w.x.xq, w.x.scale, w.x.rowsum, s);
+  const dim3 grid(M * bl::kRouteBlocks), block(bl::kRouteThreads);
+  int* clear = reinterpret_cast<int*>(w.amax);
+  // launched in full order: the kernels of a call before may still use the workspace
+  st = x_dtype == BL_BF16
+           ? launch_ex(bl::moe_route_kernel<true>, grid, block, 0, s, false, x, m.router, rb, m.D, m.E,
+                       m.top_k, m.renormalize, w.logits, w.ids, w.weights, w.xq, w.scale, clear, n_clear)
+           : launch_ex(bl::moe_route_kernel<false>, grid, block, 0, s, false, x, m.router, rb, m.D, m.E,
+                       m.top_k, m.renormalize, w.logits, w.ids, w.weights, w.xq, w.scale, clear, n_clear);
   if (st != BL_OK) return st;
-  constexpr int kRows = bl::kMoeThreads / 32 * 16;
-  bl::moe_gate_up_kernel<<<dim3((m.F + kRows - 1) / kRows, m.E), bl::kMoeThreads, 0, s>>>(
-      w.ids, w.x.xq, w.x.scale, w.x.rowsum, m.gate, m.up, m.gate_gamma, m.up_gamma, P, m.top_k, m.D, m.F,
-      m.act, w.inner);
-  st = launch_act_quant(w.inner, BL_F32, P, m.F, w.h.xq, w.h.scale, w.h.rowsum, s);
+  bl::MoeArgs a{};
+  a.ids = w.ids;
+  a.weights = w.weights;
+  a.xq = w.xq;
+  a.xscale = w.scale;
+  a.gate = m.gate;
+  a.up = m.up;
+  a.down = m.down;
+  a.gate_gamma = m.gate_gamma;
+  a.up_gamma = m.up_gamma;
+  a.down_gamma = m.down_gamma;
+  a.inner = w.inner;
+  a.amax = w.amax;
+  a.hq = w.hq;
+  a.hscale = w.hscale;
+  a.part = w.part;
+  a.M = M;
+  a.E = m.E;
+  a.D = m.D;
+  a.F = m.F;
+  a.top_k = m.top_k;
+  a.act = m.act;
+  // Columns of a run: enough for the pairs that an expert is likely to have (the mean and three
+  // deviations of independent choices); an expert with more reads its weights again.
+  const double mean = static_cast<double>(M) * m.top_k / m.E, likely = mean + 3.0 * std::sqrt(mean);
+  st = M <= 4                        ? launch_moe<1, bl::kPairs>(a, w, s)
+       : M <= 8 || likely <= 8.0     ? launch_moe<1, bl::kFour>(a, w, s)
+       : M <= 16 || likely <= 16.0   ? launch_moe<2, bl::kFour>(a, w, s)
+                                     : launch_moe<4, bl::kTwo>(a, w, s);
   if (st != BL_OK) return st;
-  bl::moe_down_kernel<<<dim3((m.D + kRows - 1) / kRows, m.E), bl::kMoeThreads, 0, s>>>(
-      w.ids, w.h.xq, w.h.scale, w.h.rowsum, m.down, m.down_gamma, P, m.D, m.F, w.part);
-  if (y_dtype == BL_BF16)
-    bl::moe_combine_kernel<true><<<dim3((m.D + 255) / 256, M), 256, 0, s>>>(w.part, w.weights, m.D, m.top_k, y);
-  else
-    bl::moe_combine_kernel<false><<<dim3((m.D + 255) / 256, M), 256, 0, s>>>(w.part, w.weights, m.D, m.top_k, y);
-  return launch_status();
+  const dim3 out((m.D + 255) / 256, M), threads(256);
+  return y_dtype == BL_BF16
+             ? launch_ex(bl::moe_combine_kernel<true>, out, threads, 0, s, true, w.part, w.weights, m.D, m.top_k, y)
+             : launch_ex(bl::moe_combine_kernel<false>, out, threads, 0, s, true, w.part, w.weights, m.D, m.top_k, y);
 }
 
 size_t bitlinear_base3_row_bytes(int K) {

@@ -33,37 +33,90 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
 // 8 n + 2 t and 8 n + 2 t + 1 of the products with fragment j. The masks are what bounds this
 // (the logic pipe takes a warp's instruction in two cycles), so the planes stay where they
 // are in the word and an accumulator per plane takes the factor 4^j.
-//   kPairs = false: fragment j is plane j, (w & 3 4^j); a column is a token. 4 masks a word.
-//   kPairs = true, for up to 4 tokens, which leave half of the 8 columns empty: fragment j is
-//     planes 0 .. j, w & (4^(j+1) - 1), so the last is the word itself and needs no mask. With
-//     P_j the products of fragment j, plane j is (P_j - P_(j-1)) / 4^j: an even column holds the
-//     token's codes of plane j, the odd one behind it those of plane j + 1, to be subtracted.
+//   kFour: fragment j is plane j, (w & 3 4^j); a column is a token. 4 masks a word.
+//   kPairs, for up to 4 tokens, which leave half of the 8 columns empty: fragment j is planes
+//     0 .. j, w & (4^(j+1) - 1), so the last is the word itself and needs no mask. With P_j the
+//     products of fragment j, plane j is (P_j - P_(j-1)) / 4^j: an even column holds the token's
+//     codes of plane j, the odd one behind it those of plane j + 1, to be subtracted.
 //     3 masks a word (70B up, one token: 15.2 -> 13.8 us with both steps).
-template <int NT, bool kPairs>
-__device__ __forceinline__ void ternary_step(int (&acc)[4][NT][4], const uint4& wa, const uint4& wb,
-                                             const uint4 (&q)[NT][4]) {
+//   kTwo: planes 2 and 3 are shifted by 4 onto 0 and 1, two accumulators instead of four, for
+//     kernels that have no registers left. 4 masks and a shift a word.
+enum PlaneMode : int { kFour = 0, kPairs = 1, kTwo = 2 };
+__host__ __device__ constexpr int planes(int mode) { return mode == kTwo ? 2 : 4; }
+
+template <int NT, int MODE>
+__device__ __forceinline__ void ternary_step(int (&acc)[planes(MODE)][NT][4], const uint4& wa,
+                                             const uint4& wb, const uint4 (&q)[NT][4]) {
 #pragma unroll
   for (int i = 0; i < 4; i += 2)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t m = kPairs ? (j == 3 ? 0xffffffffu : ((4u << (2 * j)) - 1u) * 0x01010101u)
-                                : 0x03030303u << (2 * j);
-      const uint32_t a0 = word_of(wa, i) & m, a1 = word_of(wb, i) & m;
-      const uint32_t a2 = word_of(wa, i + 1) & m, a3 = word_of(wb, i + 1) & m;
+      const int sh = (MODE == kTwo && j >= 2) ? 4 : 0;
+      const uint32_t m = MODE == kPairs ? (j == 3 ? 0xffffffffu : ((4u << (2 * j)) - 1u) * 0x01010101u)
+                         : MODE == kTwo ? 0x03030303u << (2 * (j & 1))
+                                        : 0x03030303u << (2 * j);
+      const uint32_t a0 = (word_of(wa, i) >> sh) & m, a1 = (word_of(wb, i) >> sh) & m;
+      const uint32_t a2 = (word_of(wa, i + 1) >> sh) & m, a3 = (word_of(wb, i + 1) >> sh) & m;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        mma_u8s8(acc[j][n], a0, a1, a2, a3, word_of(q[n][i], j), word_of(q[n][i + 1], j));
+        mma_u8s8(acc[MODE == kTwo ? j & 1 : j][n], a0, a1, a2, a3, word_of(q[n][i], j),
+                 word_of(q[n][i + 1], j));
     }
 }
-// The exact sum: of column e & 1 (kPairs = false), or of the token of both columns (e even).
-template <int NT, bool kPairs>
-__device__ __forceinline__ int ternary_sum(const int (&acc)[4][NT][4], int n, int e) {
-  if (kPairs)
+// The exact sum: of column e & 1, or (kPairs) of the token of both columns (e even).
+template <int NT, int MODE>
+__device__ __forceinline__ int ternary_sum(const int (&acc)[planes(MODE)][NT][4], int n, int e) {
+  if constexpr (MODE == kPairs)
     return acc[0][n][e] + ((acc[1][n][e] - acc[0][n][e + 1]) >> 2) +
            ((acc[2][n][e] - acc[1][n][e + 1]) >> 4) + ((acc[3][n][e] - acc[2][n][e + 1]) >> 6);
-  return acc[0][n][e] + (acc[1][n][e] >> 2) + (acc[2][n][e] >> 4) + (acc[3][n][e] >> 6);
+  else if constexpr (MODE == kTwo)
+    return acc[0][n][e] + (acc[1][n][e] >> 2);
+  else
+    return acc[0][n][e] + (acc[1][n][e] >> 2) + (acc[2][n][e] >> 4) + (acc[3][n][e] >> 6);
 }
-// Codes of an odd column (kPairs): those of the plane behind, none behind the last.
+// Clears the sums, minus[n] (the negative sum of codes) for the columns that u = c + 1 wants
+// it taken off: in kPairs the even ones.
+template <int NT, int MODE>
+__device__ __forceinline__ void ternary_clear(int (&acc)[planes(MODE)][NT][4], const int (&minus)[NT][2]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      acc[0][n][e] = minus[n][e & 1];
+#pragma unroll
+      for (int j = 1; j < planes(MODE); ++j) acc[j][n][e] = 0;
+    }
+}
+// minus[] from each lane's sum of the codes it loaded for token n (of column 8 n + g, or
+// (kPairs) column g).
+template <int MODE>
+__device__ __forceinline__ void minus_of(int sum, int (&minus)[2]) {
+  const int t4 = threadIdx.x & 3;
+  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+  minus[0] = -__shfl_sync(0xffffffffu, sum, 8 * t4);
+  minus[1] = -__shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
+  if (MODE == kPairs) minus[1] = 0;
+}
+__device__ __forceinline__ int dot_ones(const uint4& v, int sum) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sum = __dp4a(static_cast<int>(word_of(v, j)), 0x01010101, sum);
+  return sum;
+}
+// Adds a tile's sums of this warp to those of its block, to[row of the tile][column], for the
+// columns below `valid`.
+template <int NT, int MODE>
+__device__ __forceinline__ void ternary_add(const int (&acc)[planes(MODE)][NT][4], int* to, int valid) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; e += MODE == kPairs ? 2 : 1) {
+      const int t = MODE == kPairs ? t4 : 8 * n + 2 * t4 + (e & 1);
+      if (t < valid) atomicAdd(to + (g + (e < 2 ? 0 : 8)) * 8 * NT + t, ternary_sum<NT, MODE>(acc, n, e));
+    }
+}
+// Codes of an odd column in kPairs: those of the plane behind, none behind the last.
 __device__ __forceinline__ uint4 next_plane(const uint4& v) { return make_uint4(v.y, v.z, v.w, 0u); }
 
 constexpr int kFewMaxWarps = 8;     // warps of a block
@@ -74,7 +127,7 @@ constexpr int kFewRound = 32;       // tiles of 16 rows between two joins of the
 __host__ __device__ constexpr int few_depth(int NT) { return NT == 1 ? 12 : 8; }
 // Steps of a warp: as many as its registers hold codes for (fewer steps per warp mean more
 // sums to join for the same weights: one token, 70B up, 1 / 2 / 4 steps: 17.8 / 15.8 / 13.9 us).
-__host__ __device__ constexpr int few_steps(int NT) { return NT == 1 ? 4 : 2; }
+__host__ __device__ constexpr int few_steps(int NT) { return 4 / NT; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -132,8 +185,8 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int t) {
   exchange(v[2], v[3], t & 1, 1);
 }
 
-// y[t,n] = fl(float(sum_k c q) fl(scale_t gamma)) for M <= 8 NT tokens (4 with kPairs). Bound by the packed
-// weights' bytes. K is split over all warps of a cluster of blocks, few_steps steps of 256 to one,
+// y[t,n] = fl(float(sum_k c q) fl(scale_t gamma)) for M <= 8 NT tokens (4 in
+// kPairs). Bound by the packed weights' bytes. K is split over all warps of a cluster of blocks, few_steps steps of 256 to one,
 // so that a warp can keep its part of every token in registers for the whole kernel: the
 // codes are read once per cluster, not once per block (they are the same lines for
 // everybody, and L2 hands out one line at a time), and the loop has no shared-memory reads.
@@ -143,7 +196,7 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int t) {
 // before the join. The ring holds what the memory delivers while the codes arrive. The stream has no bounds to check: rows past N and
 // chunks past K read the last ones, and meet outputs that are not written and codes that
 // are zero.
-template <int NT, bool kPairs, bool kOBf16>
+template <int NT, int MODE, bool kOBf16>
 __global__ void __launch_bounds__(32 * kFewMaxWarps, 2) few_tokens_kernel(
     const int8_t* __restrict__ xq, const float* __restrict__ scale, const uint8_t* __restrict__ packed,
     const float* __restrict__ gamma_ptr, void* __restrict__ y, int M, int N, int K, int cs) {
@@ -186,7 +239,7 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 2) few_tokens_kernel(
   int minus[NT][2];  // -sum of the warp's codes of the tokens of this lane's columns
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int t = kPairs ? g >> 1 : 8 * n + g;
+    const int t = MODE == kPairs ? g >> 1 : 8 * n + g;
     const uint4* row = reinterpret_cast<const uint4*>(xq + static_cast<size_t>(min(t, M - 1)) * K);
     int sum = 0;
 #pragma unroll
@@ -203,15 +256,11 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 2) few_tokens_kernel(
       if (NT > 1) transpose4(v, t4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum = __dp4a(static_cast<int>(word_of(v[i], j)), 0x01010101, sum);
-        q[s][n][i] = kPairs && (g & 1) ? next_plane(v[i]) : v[i];
+        sum = dot_ones(v[i], sum);
+        q[s][n][i] = MODE == kPairs && (g & 1) ? next_plane(v[i]) : v[i];
       }
     }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    minus[n][0] = -__shfl_sync(0xffffffffu, sum, 8 * t4);
-    minus[n][1] = kPairs ? 0 : -__shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
+    minus_of<MODE>(sum, minus[n]);
   }
   if (threadIdx.x < M) factor[threadIdx.x] = __fmul_rn(scale[threadIdx.x], *gamma_ptr);
   __syncthreads();  // the sums are zero
@@ -219,30 +268,17 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 2) few_tokens_kernel(
   for (int i0 = 0; i0 < count; i0 += kFewRound) {
     const int i1 = min(count, i0 + kFewRound);
     for (int i = i0; i < i1; ++i) {
-      int acc[4][NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          acc[0][n][e] = minus[n][e & 1];
-          acc[1][n][e] = acc[2][n][e] = acc[3][n][e] = 0;
-        }
+      int acc[planes(MODE)][NT][4];
+      ternary_clear<NT, MODE>(acc, minus);
       cp_async_wait<kAhead - 1>();
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         const uint4 wa = ld_shared_v4(slot + s * 1024), wb = ld_shared_v4(slot + s * 1024 + 512);
-        ternary_step<NT, kPairs>(acc, wa, wb, q[s]);
+        ternary_step<NT, MODE>(acc, wa, wb, q[s]);
       }
       fetch(slot, i + kAhead);
       slot = slot + S * 1024 == ring + kAhead * S * 1024 ? ring : slot + S * 1024;
-      int* to = sums + ((i - i0) * 16 + g) * 8 * NT;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; e += kPairs ? 2 : 1) {
-          const int t = kPairs ? t4 : 8 * n + 2 * t4 + (e & 1);
-          if (t < M) atomicAdd(to + (e < 2 ? 0 : 64 * NT) + t, ternary_sum<NT, kPairs>(acc, n, e));
-        }
+      ternary_add<NT, MODE>(acc, sums + (i - i0) * 16 * 8 * NT, M);
     }
     if (cs > 1) cluster_barrier(); else __syncthreads();
     // The cluster's blocks share the tiles of the round; a thread takes four tokens of a row.

@@ -14,7 +14,6 @@ namespace bl {
 constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxExperts = 512;
 constexpr int kMoeMaxTopK = 16;
-constexpr int kMoeThreads = 128;
 
 enum MoeAct : int { kActSilu = 0, kActRelu2 = 1 };
 
@@ -42,6 +41,8 @@ __device__ __forceinline__ void moe_top_k(const float* logits, int E, int top_k,
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
+    key[i] = 0u;
+    if (32 * i >= E) continue;
     const int e = 32 * i + lane;
     const float v = e < E ? logits[e] : 0.0f;
     bad |= !(fabsf(v) <= kFloatMax);
@@ -56,7 +57,7 @@ __device__ __forceinline__ void moe_top_k(const float* logits, int E, int top_k,
     uint32_t e = 0xffffffffu;
 #pragma unroll
     for (int i = kPer - 1; i >= 0; --i)
-      if (key[i] == k) e = 32 * i + lane;
+      if (32 * i < E && key[i] == k) e = 32 * i + lane;
     e = __reduce_min_sync(0xffffffffu, e);
     const float v = logits[e];
     if (s == 0) top = v;
@@ -66,6 +67,7 @@ __device__ __forceinline__ void moe_top_k(const float* logits, int E, int top_k,
     best = 0u;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
+      if (32 * i >= E) continue;
       if (32u * i + lane == e) key[i] = 0u;
       best = max(best, key[i]);
     }
@@ -80,128 +82,322 @@ __device__ __forceinline__ void moe_top_k(const float* logits, int E, int top_k,
   }
 }
 
-// Logits and choice of one token per block, a warp per expert in turn.
+// ------------------------------------------------------------------------------- route
+// One cluster of 8 blocks per token. Each block takes an eighth of the experts' logits (a warp
+// per expert in turn), quantizes an eighth of the row, and the first one chooses. Also clears
+// what the next two kernels count in. Bound by latency (the router's rows come from L2 for
+// all but the first tokens); one block per token would read all of the router alone.
+constexpr int kRouteThreads = 256;
+constexpr int kRouteBlocks = 8;
+
 template <bool kXBf16>
-__global__ void __launch_bounds__(256) moe_route_kernel(
-    const void* __restrict__ x, const void* __restrict__ router, int r_bf16, int D, int E, int top_k,
-    int renorm, int* __restrict__ ids, float* __restrict__ weights) {
+__global__ void __launch_bounds__(kRouteThreads) __cluster_dims__(kRouteBlocks, 1, 1)
+moe_route_kernel(const void* __restrict__ x, const void* __restrict__ router, int r_bf16, int D, int E,
+                 int top_k, int renorm, float* logits_all, int* __restrict__ ids,
+                 float* __restrict__ weights, int8_t* __restrict__ xq, float* __restrict__ xscale,
+                 int* __restrict__ clear, int n_clear) {
   __shared__ float logits[kMoeMaxExperts];
-  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  allow_dependent_launch();
+  const int t = blockIdx.x / kRouteBlocks, part = blockIdx.x % kRouteBlocks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = blockIdx.x * kRouteThreads + threadIdx.x; i < n_clear; i += gridDim.x * kRouteThreads) clear[i] = 0;
   const char* xr = static_cast<const char*>(x) + row_offset(t, D, kXBf16);
-  for (int e = warp; e < E; e += 8) {
-    const char* rr = static_cast<const char*>(router) + row_offset(e, D, r_bf16);
+  float* mine = logits_all + static_cast<size_t>(t) * E;
+  float m = 0.0f;
+  bool bad = false;
+  // every warp reads the whole row, for its first expert's logit (or none) and the maximum
+  for (int e = part + kRouteBlocks * warp; e < E || e == part + kRouteBlocks * warp;
+       e += kRouteBlocks * kRouteThreads / 32) {
+    const char* rr = static_cast<const char*>(router) + row_offset(min(e, E - 1), D, r_bf16);
     float s = 0.0f;
+#pragma unroll 4
     for (int c = lane; c < D / 8; c += 32) {
       float a[8], b[8];
       load8<kXBf16>(xr, c, a);
       load8_any(rr, r_bf16, c, b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
+      for (int i = 0; i < 8; ++i) {
+        s = fmaf(a[i], b[i], s);
+        bad |= !(fabsf(a[i]) <= kFloatMax);
+        m = fmaxf(m, fabsf(a[i]));
+      }
     }
     s = warp_sum(s);
-    if (lane == 0) logits[e] = s;
+    if (lane == 0 && e < E) __stcg(mine + e, s);
   }
+  if (bad) record_status(kStatusNonfinite);
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  const float f = m > 0.0f ? __fdiv_rn(127.0f, m) : 0.0f;
+  for (int c = part * kRouteThreads + threadIdx.x; c < D / 8; c += kRouteBlocks * kRouteThreads) {
+    float v[8];
+    load8<kXBf16>(xr, c, v);
+    uint32_t q[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      q[i >> 2] |= (static_cast<uint32_t>(quant_i8(v[i], f)) & 0xffu) << (8 * (i & 3));
+    reinterpret_cast<uint2*>(xq + static_cast<size_t>(t) * D)[c] = make_uint2(q[0], q[1]);
+  }
+  cluster_barrier();  // the logits of the other blocks
+  if (part != 0) return;
+  if (threadIdx.x == 0) xscale[t] = m > 0.0f ? __fdiv_rn(m, 127.0f) : 0.0f;
+  for (int e = threadIdx.x; e < E; e += kRouteThreads) logits[e] = __ldcg(mine + e);
   __syncthreads();
   if (warp == 0) moe_top_k(logits, E, top_k, renorm, ids + t * top_k, weights + t * top_k);
 }
 
-// The pairs of one expert, in order, into list; their number. Called by a whole block.
-__device__ __forceinline__ int moe_pairs_of(const int* __restrict__ ids, int pairs, int expert,
-                                            int* list, int* count) {
+// ------------------------------------------------------------------------------- experts
+constexpr int kMoeThreads = 256;
+constexpr int kMoeWarps = kMoeThreads / 32;
+constexpr int kMoeRingBytes = 8 * 1024;    // weights a warp keeps in flight
+constexpr int kMoeSumBytes = 32 * 1024;    // integer sums of a run
+
+// The pairs by expert: block-wide, in shared memory.
+struct MoeGroups {
+  int active;                       // experts with a pair
+  int expert[kMoeMaxExperts];       // their indexes, ascending
+  int begin[kMoeMaxExperts + 1];    // their pairs are list[begin[a] .. begin[a + 1])
+  short list[kMoeMaxTokens * kMoeMaxTopK];
+  int cursor[kMoeMaxExperts];
+};
+
+__device__ __forceinline__ void moe_group(MoeGroups& g, const int* ids, int pairs, int E) {
+  constexpr int kPer = kMoeMaxTokens * kMoeMaxTopK / kMoeThreads;
+  int mine[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int p = i * kMoeThreads + threadIdx.x;
+    mine[i] = p < pairs ? __ldcg(ids + p) : -1;
+  }
+  for (int e = threadIdx.x; e < E; e += kMoeThreads) g.cursor[e] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (mine[i] >= 0) atomicAdd(&g.cursor[mine[i]], 1);
+  __syncthreads();
   if (threadIdx.x < 32) {
-    int n = 0;
-    for (int p0 = 0; p0 < pairs; p0 += 32) {
-      const int p = p0 + static_cast<int>(threadIdx.x);
-      const bool is = p < pairs && ids[p] == expert;
-      const uint32_t b = __ballot_sync(0xffffffffu, is);
-      if (is) list[n + __popc(b & ((1u << threadIdx.x) - 1u))] = p;
-      n += __popc(b);
+    const int lane = threadIdx.x;
+    int a0 = 0, p0 = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane, n = e < E ? g.cursor[e] : 0;
+      const uint32_t has = __ballot_sync(0xffffffffu, n > 0);
+      int before = n;  // pairs of the lanes up to this one
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+      }
+      if (n > 0) {
+        const int a = a0 + __popc(has & ((1u << lane) - 1u));
+        g.expert[a] = e;
+        g.begin[a] = p0 + before - n;
+        g.cursor[e] = p0 + before - n;
+      }
+      a0 += __popc(has);
+      p0 += __shfl_sync(0xffffffffu, before, 31);
     }
-    if (threadIdx.x == 0) *count = n;
+    if (lane == 0) {
+      g.active = a0;
+      g.begin[a0] = p0;
+    }
   }
   __syncthreads();
-  return *count;
-}
-
-// One 16-row tile of `rows` against up to 8 pairs of codes (pair list[i0 + g] reads row
-// list[...] / div of q).
-__device__ __forceinline__ void moe_tile(int (&acc)[4][1][4], const uint8_t* __restrict__ w, int row0,
-                                         int K, const int8_t* __restrict__ q, const int8_t* qrow) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3, chunks = K / 64;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  const uint4* pa = reinterpret_cast<const uint4*>(w + static_cast<size_t>(row0 + g) * (K / 4));
-  const uint4* pb = reinterpret_cast<const uint4*>(w + static_cast<size_t>(row0 + g + 8) * (K / 4));
-  for (int c = t4; c - t4 < chunks; c += 4) {
-    const bool in = c < chunks;
-    const uint4 wa = in ? ld_stream_v4(pa + c) : zero, wb = in ? ld_stream_v4(pb + c) : zero;
-    uint4 v[1][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[0][i] = (in && qrow) ? reinterpret_cast<const uint4*>(qrow)[4 * c + i] : zero;
-    ternary_step<1, false>(acc, wa, wb, v);
-  }
+  for (int i = 0; i < kPer; ++i)
+    if (mine[i] >= 0)
+      g.list[atomicAdd(&g.cursor[mine[i]], 1)] = static_cast<short>(i * kMoeThreads + threadIdx.x);
+  __syncthreads();
 }
 
-// inner[p][f] = act(G) * U for the pairs of expert blockIdx.y; a warp per 16 rows.
-__global__ void __launch_bounds__(kMoeThreads) moe_gate_up_kernel(
-    const int* __restrict__ ids, const int8_t* __restrict__ xq, const float* __restrict__ xscale,
-    const int* __restrict__ xsum, const uint8_t* __restrict__ gate, const uint8_t* __restrict__ up,
-    const float* __restrict__ gate_gamma, const float* __restrict__ up_gamma, int pairs, int top_k,
-    int D, int F, int act, float* __restrict__ inner) {
-  __shared__ int list[kMoeMaxTokens];
-  __shared__ int count;
-  const int e = blockIdx.y;
-  const int n = moe_pairs_of(ids, pairs, e, list, &count);
+// Everything that the two expert kernels read and write.
+struct MoeArgs {
+  const int* ids;         // [pairs]
+  const float* weights;   // [pairs]
+  const int8_t* xq;       // [M][D]
+  const float* xscale;    // [M]
+  const uint8_t *gate, *up, *down;
+  const float *gate_gamma, *up_gamma, *down_gamma;
+  float* inner;           // [pairs][F]
+  unsigned* amax;         // [pairs] bits of the largest |inner|; starts at 0
+  const int8_t* hq;       // [pairs][F] codes of inner
+  const float* hscale;    // [pairs]
+  float* part;            // [pairs][D] the experts' outputs
+  int M, E, D, F, top_k, act;
+  int wk, passes;         // warps of a block along K, and turns of all of them
+};
+
+// A run: up to kRunTiles tiles of one expert, for one group of 8 NT of its pairs.
+struct MoeRun {
+  int pos, a, tile, tiles, group, groups;
+};
+
+// The 16-row tiles of the active experts, in order, are dealt out in equal stretches to the blocks,
+// two per SM (one's barriers and loads of codes hide behind the other's stream). Within a
+// block wk warps split K and the others take further tiles. As in few_tokens_kernel a warp
+// holds its part of the codes in registers, streams its weights through a ring of its own that
+// runs ahead across tiles and runs, and adds its sums to the block's; a run ends with a
+// barrier, where they become
+//   kDown = false: inner = act(G) U of the run's rows and pairs, and their maximum;
+//   kDown = true:  the experts' outputs.
+template <int NT, int MODE, bool kDown>
+__global__ void __launch_bounds__(kMoeThreads, 2) moe_expert_kernel(const MoeArgs p) {
+  constexpr int S = few_steps(NT), kMats = kDown ? 1 : 2;
+  constexpr int kAhead = kMoeRingBytes / 1024 / S;
+  constexpr int kCols = 8 * NT;
+  constexpr int kRunTiles = kMoeSumBytes / (kMats * 16 * kCols * 4);
+  extern __shared__ __align__(16) uint8_t ring_all[];  // then the sums [matrix][row of the run][column]
+  int* sums = reinterpret_cast<int*>(ring_all + kMoeWarps * kMoeRingBytes);
+  __shared__ MoeGroups groups;
+  __shared__ unsigned top[kCols];
+  __shared__ float factor[kMats][kCols];  // scale of a pair's codes times gamma
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const int row0 = (blockIdx.x * (kMoeThreads / 32) + warp) * 16;
-  if (row0 >= F) return;
-  const size_t per = static_cast<size_t>(F) * (D / 4);
-  const float gg = gate_gamma[e], gu = up_gamma[e];
-  for (int i0 = 0; i0 < n; i0 += 8) {
-    const int8_t* qrow = i0 + g < n ? xq + static_cast<size_t>(list[i0 + g] / top_k) * D : nullptr;
-    int ag[4][1][4] = {}, au[4][1][4] = {};
-    moe_tile(ag, gate + e * per, row0, D, xq, qrow);
-    moe_tile(au, up + e * per, row0, D, xq, qrow);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = i0 + 2 * t4 + (j & 1);
-      if (i < n) {
-        const int p = list[i], t = p / top_k;
-        const float s = xscale[t];
-        const float G = __fmul_rn(__int2float_rn(ternary_sum<1, false>(ag, 0, j) - xsum[t]), __fmul_rn(s, gg));
-        const float U = __fmul_rn(__int2float_rn(ternary_sum<1, false>(au, 0, j) - xsum[t]), __fmul_rn(s, gu));
-        inner[static_cast<size_t>(p) * F + row0 + g + (j < 2 ? 0 : 8)] = __fmul_rn(moe_act(G, act), U);
+  const int N = kDown ? p.D : p.F, K = kDown ? p.F : p.D, pairs = p.M * p.top_k;
+  const int chunks = K / 64, per = N / 16;  // tiles of an expert (N % 64 == 0)
+  const int wr = warp / p.wk, WR = kMoeWarps / p.wk, wk = warp % p.wk;
+  const size_t pitch = static_cast<size_t>(K / 4), matrix = static_cast<size_t>(N) * pitch;
+  for (int i = threadIdx.x; i < kMoeSumBytes / 16; i += kMoeThreads)
+    reinterpret_cast<uint4*>(sums)[i] = make_uint4(0u, 0u, 0u, 0u);
+  // The pairs were chosen by the kernel before the gate and up products, which let this one
+  // start only after it had waited for that: the down kernel may read them at once.
+  if (!kDown) grid_dependency_wait();
+  moe_group(groups, p.ids, pairs, p.E);
+  if (!kDown) allow_dependent_launch();
+  const long long total = static_cast<long long>(groups.active) * per;
+  const int end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
+  auto start = [&](MoeRun& r, int pos) {
+    r.pos = pos;
+    if (pos >= end) return;
+    r.a = pos / per;
+    r.tile = pos - r.a * per;
+    r.tiles = min(min(end - pos, per - r.tile), kRunTiles);
+    r.group = 0;
+    const int n = groups.begin[r.a + 1] - groups.begin[r.a];
+    r.groups = MODE == kPairs ? 1 : (n + kCols - 1) / kCols;
+  };
+  auto next = [&](MoeRun& r) {
+    if (++r.group >= r.groups) start(r, r.pos + r.tiles);
+  };
+  // ---- the stream: units (run, turn, tile, matrix) in the order in which they are used
+  MoeRun fr;
+  int f_turn = 0, f_tile = wr, f_mat = 0;
+  start(fr, static_cast<int>(total * blockIdx.x / gridDim.x));
+  MoeRun run = fr;
+  const uint32_t ring = smem_u32(ring_all) + warp * kMoeRingBytes + lane * 16;
+  auto fetch = [&](uint32_t slot) {
+    while (fr.pos < end && f_tile >= fr.tiles) {  // runs with fewer tiles than warps
+      f_tile = wr;
+      if (++f_turn >= p.passes) {
+        f_turn = 0;
+        next(fr);
       }
     }
-  }
-}
-
-// part[p][d] = the down projection of pair p.
-__global__ void __launch_bounds__(kMoeThreads) moe_down_kernel(
-    const int* __restrict__ ids, const int8_t* __restrict__ hq, const float* __restrict__ hscale,
-    const int* __restrict__ hsum, const uint8_t* __restrict__ down, const float* __restrict__ down_gamma,
-    int pairs, int D, int F, float* __restrict__ part) {
-  __shared__ int list[kMoeMaxTokens];
-  __shared__ int count;
-  const int e = blockIdx.y;
-  const int n = moe_pairs_of(ids, pairs, e, list, &count);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const int row0 = (blockIdx.x * (kMoeThreads / 32) + warp) * 16;
-  if (row0 >= D) return;
-  const float gd = down_gamma[e];
-  for (int i0 = 0; i0 < n; i0 += 8) {
-    const int8_t* qrow = i0 + g < n ? hq + static_cast<size_t>(list[i0 + g]) * F : nullptr;
-    int acc[4][1][4] = {};
-    moe_tile(acc, down + e * (static_cast<size_t>(D) * (F / 4)), row0, F, hq, qrow);
+    if (fr.pos < end) {
+      const uint8_t* w = kDown ? p.down : f_mat ? p.up : p.gate;
+      const int c = 4 * S * (f_turn * p.wk + wk) + t4;
+      const uint8_t* a = w + groups.expert[fr.a] * matrix + ((fr.tile + f_tile) * 16 + g) * pitch;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = i0 + 2 * t4 + (j & 1);
-      if (i < n) {
-        const int p = list[i];
-        part[static_cast<size_t>(p) * D + row0 + g + (j < 2 ? 0 : 8)] =
-            __fmul_rn(__int2float_rn(ternary_sum<1, false>(acc, 0, j) - hsum[p]), __fmul_rn(hscale[p], gd));
+      for (int s = 0; s < S; ++s) {
+        const int at = 16 * min(c + 4 * s, chunks - 1);
+        cp_async16(slot + s * 1024, a + at);
+        cp_async16(slot + s * 1024 + 512, a + 8 * pitch + at);
+      }
+      if (++f_mat == kMats) {
+        f_mat = 0;
+        f_tile += WR;
       }
     }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(ring + i * S * 1024);
+  if (kDown) grid_dependency_wait();
+  // ---- the runs
+  uint4 q[S][NT][4];
+  int minus[NT][2];
+  int held_a = -1, held_group = -1;
+  uint32_t slot = ring;
+  while (run.pos < end) {
+    const int e = groups.expert[run.a], first = groups.begin[run.a] + run.group * kCols;
+    const int n = min(groups.begin[run.a + 1] - first, kCols);  // pairs of the group
+    if (threadIdx.x < n) {  // read behind the barrier that ends the run's products
+      const int pair = groups.list[first + threadIdx.x];
+      if (kDown) {
+        factor[0][threadIdx.x] = __fmul_rn(p.hscale[pair], p.down_gamma[e]);
+      } else {
+        const float s = p.xscale[pair / p.top_k];
+        factor[0][threadIdx.x] = __fmul_rn(s, p.gate_gamma[e]);
+        factor[kMats - 1][threadIdx.x] = __fmul_rn(s, p.up_gamma[e]);
+        top[threadIdx.x] = 0u;
+      }
+    }
+    for (int turn = 0; turn < p.passes; ++turn) {
+      if (p.passes > 1 || held_a != run.a || held_group != run.group) {
+        held_a = run.a;
+        held_group = run.group;
+        const int c = 4 * S * (turn * p.wk + wk) + t4;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int col = MODE == kPairs ? g >> 1 : 8 * j + g;
+          const bool here = col < n;
+          const int pair = here ? groups.list[first + col] : 0;
+          int sum = 0;
+          const uint4* row = reinterpret_cast<const uint4*>(
+              (kDown ? p.hq : p.xq) + static_cast<size_t>(kDown ? pair : pair / p.top_k) * K);
+#pragma unroll
+          for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 v = (here && c + 4 * s < chunks) ? row[4 * (c + 4 * s) + i]
+                                                           : make_uint4(0u, 0u, 0u, 0u);
+              sum = dot_ones(v, sum);
+              q[s][j][i] = MODE == kPairs && (g & 1) ? next_plane(v) : v;
+            }
+          minus_of<MODE>(sum, minus[j]);
+        }
+      }
+      for (int i = wr; i < run.tiles; i += WR)
+#pragma unroll 1
+        for (int m = 0; m < kMats; ++m) {
+          int acc[planes(MODE)][NT][4];
+          ternary_clear<NT, MODE>(acc, minus);
+          cp_async_wait<kAhead - 1>();
+#pragma unroll
+          for (int s = 0; s < S; ++s) {
+            const uint4 wa = ld_shared_v4(slot + s * 1024), wb = ld_shared_v4(slot + s * 1024 + 512);
+            ternary_step<NT, MODE>(acc, wa, wb, q[s]);
+          }
+          fetch(slot);
+          slot = slot + S * 1024 == ring + kAhead * S * 1024 ? ring : slot + S * 1024;
+          ternary_add<NT, MODE>(acc, sums + (m * kRunTiles + i) * 16 * kCols, n);
+        }
+    }
+    __syncthreads();
+    // ---- the join: 16 threads take the rows of a tile for one pair
+    for (int u = threadIdx.x >> 4; u < run.tiles * n; u += kMoeThreads / 16) {
+      const int r = threadIdx.x & 15, i = u / n, col = u - i * n;
+      const int pair = groups.list[first + col], row = (run.tile + i) * 16 + r;
+      int* from = sums + (i * 16 + r) * kCols + col;
+      if (kDown) {
+        p.part[static_cast<size_t>(pair) * N + row] = __fmul_rn(__int2float_rn(*from), factor[0][col]);
+      } else {
+        int* from_up = from + kRunTiles * 16 * kCols;
+        const float G = __fmul_rn(__int2float_rn(*from), factor[0][col]);
+        const float U = __fmul_rn(__int2float_rn(*from_up), factor[kMats - 1][col]);
+        const float v = __fmul_rn(moe_act(G, p.act), U);
+        *from_up = 0;
+        p.inner[static_cast<size_t>(pair) * N + row] = v;
+        unsigned most = __float_as_uint(fabsf(v));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffu << (lane & 16), most, o));
+        if (r == 0) atomicMax(&top[col], most);
+      }
+      *from = 0;
+    }
+    __syncthreads();
+    if (!kDown) {
+      if (threadIdx.x < n) atomicMax(p.amax + groups.list[first + threadIdx.x], top[threadIdx.x]);
+      __syncwarp();  // top and factor are written again by the same threads
+    }
+    next(run);
   }
 }
 
@@ -210,9 +406,11 @@ template <bool kOBf16>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const float* __restrict__ part,
                                                          const float* __restrict__ weights, int D,
                                                          int top_k, void* __restrict__ y) {
+  grid_dependency_wait();
   const int t = blockIdx.y, d = blockIdx.x * 256 + threadIdx.x;
   if (d >= D) return;
   float s = 0.0f;
+#pragma unroll 4
   for (int k = 0; k < top_k; ++k)
     s = fmaf(weights[t * top_k + k], part[static_cast<size_t>(t * top_k + k) * D + d], s);
   const size_t at = static_cast<size_t>(t) * D + d;
