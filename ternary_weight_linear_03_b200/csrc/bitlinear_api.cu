@@ -1329,21 +1329,40 @@ MoeWs moe_ws_layout(void* base, int M, const bl_moe& m) {
   return w;
 }
 
-template <int NT, int MODE, bool kDown>
-bl_status launch_moe_expert(bl::MoeArgs a, cudaStream_t s) {
-  auto kern = bl::moe_expert_kernel<NT, MODE, kDown>;
+template <int NT, int S, int MODE, bool kDown>
+bl_status launch_moe_expert_s(const bl::MoeArgs& a, int grid, cudaStream_t s) {
+  auto kern = bl::moe_expert_kernel<NT, S, MODE, kDown>;
   constexpr int kSmem = bl::kMoeWarps * bl::kMoeRingBytes + bl::kMoeSumBytes;
   static bl::PerDevice configured;
   if (!set_smem_limit_once(configured, kern, kSmem)) return BL_ERR_CUDA;
-  const int per_warp = 256 * bl::few_steps(NT), K = kDown ? a.F : a.D;
-  const int along = (K + per_warp - 1) / per_warp;
-  for (a.wk = 1; a.wk < along && a.wk < bl::kMoeWarps; a.wk *= 2) {
-  }
-  a.passes = (along + a.wk - 1) / a.wk;
-  // no more blocks than tiles of the experts that can have a token
+  return launch_ex(kern, dim3(grid), dim3(bl::kMoeThreads), kSmem, s, true, a);
+}
+
+// Chooses how the warps of a block share K (wk of them, S steps each, in `passes` turns): the
+// shortest time of a warp, its turns over the tiles of its block times their steps, if every
+// expert that can have a token has one; of equals the fewest turns (each loads codes).
+template <int NT, int MODE, bool kDown>
+bl_status launch_moe_expert(bl::MoeArgs a, cudaStream_t s) {
+  constexpr int kMost = bl::few_steps(NT);  // kMost or kMost - 1 steps a warp
+  const int steps = ((kDown ? a.F : a.D) + 255) / 256;
   const long long tiles = static_cast<long long>(std::min(a.E, a.M * a.top_k)) * ((kDown ? a.D : a.F) / 16);
   const int grid = static_cast<int>(std::min<long long>(tiles, 2ll * num_sms()));
-  return launch_ex(kern, dim3(grid), dim3(bl::kMoeThreads), kSmem, s, true, a);
+  const long long mine = (tiles + grid - 1) / grid;
+  int S = 0;
+  long long best = 0;
+  for (int wk = 1; wk <= bl::kMoeWarps; wk *= 2)
+    for (int n = kMost; n >= kMost - 1; --n) {
+      const int passes = (steps + wk * n - 1) / (wk * n), rows = bl::kMoeWarps / wk;
+      const long long cost = ((mine + rows - 1) / rows * passes * n) * 64 + passes;
+      if (S == 0 || cost < best) {
+        best = cost;
+        S = n;
+        a.wk = wk;
+        a.passes = passes;
+      }
+    }
+  return S == kMost ? launch_moe_expert_s<NT, kMost, MODE, kDown>(a, grid, s)
+                    : launch_moe_expert_s<NT, kMost - 1, MODE, kDown>(a, grid, s);
 }
 
 // The gate and up products, the codes of what comes out, the down products.
@@ -1441,16 +1460,19 @@ bl_status bitlinear_moe_forward(const void* x, int x_dtype, int M, const bl_moe*
   const bl_moe& m = *layer;
   if (!ws || ws_bytes < moe_ws_layout(nullptr, M, m).bytes) return BL_ERR_WORKSPACE;
   const MoeWs w = moe_ws_layout(ws, M, m);
-  const int rb = m.router_dtype == BL_BF16 ? 1 : 0, n_clear = M * m.top_k;
+  const int n_clear = M * m.top_k;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid(M * bl::kRouteBlocks), block(bl::kRouteThreads);
   int* clear = reinterpret_cast<int*>(w.amax);
   // launched in full order: the kernels of a call before may still use the workspace
-  st = x_dtype == BL_BF16
-           ? launch_ex(bl::moe_route_kernel<true>, grid, block, 0, s, false, x, m.router, rb, m.D, m.E,
-                       m.top_k, m.renormalize, w.logits, w.ids, w.weights, w.xq, w.scale, clear, n_clear)
-           : launch_ex(bl::moe_route_kernel<false>, grid, block, 0, s, false, x, m.router, rb, m.D, m.E,
-                       m.top_k, m.renormalize, w.logits, w.ids, w.weights, w.xq, w.scale, clear, n_clear);
+  auto route = [&](auto kern) {
+    return launch_ex(kern, grid, block, 0, s, false, x, m.router, m.D, m.E, m.top_k, m.renormalize,
+                     w.logits, w.ids, w.weights, w.xq, w.scale, clear, n_clear);
+  };
+  if (x_dtype == BL_BF16)
+    st = m.router_dtype == BL_BF16 ? route(bl::moe_route_kernel<true, true>) : route(bl::moe_route_kernel<true, false>);
+  else
+    st = m.router_dtype == BL_BF16 ? route(bl::moe_route_kernel<false, true>) : route(bl::moe_route_kernel<false, false>);
   if (st != BL_OK) return st;
   bl::MoeArgs a{};
   a.ids = w.ids;
@@ -1474,13 +1496,12 @@ bl_status bitlinear_moe_forward(const void* x, int x_dtype, int M, const bl_moe*
   a.F = m.F;
   a.top_k = m.top_k;
   a.act = m.act;
-  // Columns of a run: enough for the pairs that an expert is likely to have (the mean and three
-  // deviations of independent choices); an expert with more reads its weights again.
-  const double mean = static_cast<double>(M) * m.top_k / m.E, likely = mean + 3.0 * std::sqrt(mean);
-  st = M <= 4                        ? launch_moe<1, bl::kPairs>(a, w, s)
-       : M <= 8 || likely <= 8.0     ? launch_moe<1, bl::kFour>(a, w, s)
-       : M <= 16 || likely <= 16.0   ? launch_moe<2, bl::kFour>(a, w, s)
-                                     : launch_moe<4, bl::kTwo>(a, w, s);
+  // 16 columns where an expert is likely to have more than 8 tokens (the mean and two deviations
+  // of independent choices); one with more than the columns reads its weights again, from L2.
+  const double mean = static_cast<double>(M) * m.top_k / m.E;
+  st = M <= 4                                          ? launch_moe<1, bl::kPairs>(a, w, s)
+       : M <= 8 || mean + 2.0 * std::sqrt(mean) <= 8.0 ? launch_moe<1, bl::kFour>(a, w, s)
+                                                       : launch_moe<2, bl::kFour>(a, w, s);
   if (st != BL_OK) return st;
   const dim3 out((m.D + 255) / 256, M), threads(256);
   return y_dtype == BL_BF16

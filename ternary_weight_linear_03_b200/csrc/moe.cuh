@@ -90,9 +90,9 @@ __device__ __forceinline__ void moe_top_k(const float* logits, int E, int top_k,
 constexpr int kRouteThreads = 256;
 constexpr int kRouteBlocks = 8;
 
-template <bool kXBf16>
+template <bool kXBf16, bool kRBf16>
 __global__ void __launch_bounds__(kRouteThreads) __cluster_dims__(kRouteBlocks, 1, 1)
-moe_route_kernel(const void* __restrict__ x, const void* __restrict__ router, int r_bf16, int D, int E,
+moe_route_kernel(const void* __restrict__ x, const void* __restrict__ router, int D, int E,
                  int top_k, int renorm, float* logits_all, int* __restrict__ ids,
                  float* __restrict__ weights, int8_t* __restrict__ xq, float* __restrict__ xscale,
                  int* __restrict__ clear, int n_clear) {
@@ -108,18 +108,26 @@ moe_route_kernel(const void* __restrict__ x, const void* __restrict__ router, in
   // every warp reads the whole row, for its first expert's logit (or none) and the maximum
   for (int e = part + kRouteBlocks * warp; e < E || e == part + kRouteBlocks * warp;
        e += kRouteBlocks * kRouteThreads / 32) {
-    const char* rr = static_cast<const char*>(router) + row_offset(min(e, E - 1), D, r_bf16);
+    const char* rr = static_cast<const char*>(router) + row_offset(min(e, E - 1), D, kRBf16);
     float s = 0.0f;
-#pragma unroll 4
-    for (int c = lane; c < D / 8; c += 32) {
-      float a[8], b[8];
-      load8<kXBf16>(xr, c, a);
-      load8_any(rr, r_bf16, c, b);
+    constexpr int kBatch = 4;  // vectors in flight per lane: one trip to L2 for four
+    for (int c0 = lane; c0 < D / 8; c0 += kBatch * 32) {
+      float a[kBatch][8], b[kBatch][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s = fmaf(a[i], b[i], s);
-        bad |= !(fabsf(a[i]) <= kFloatMax);
-        m = fmaxf(m, fabsf(a[i]));
+      for (int u = 0; u < kBatch; ++u) {
+        const int c = min(c0 + 32 * u, D / 8 - 1);
+        load8<kXBf16>(xr, c, a[u]);
+        load8<kRBf16>(rr, c, b[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const bool in = c0 + 32 * u < D / 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s = fmaf(a[u][i], in ? b[u][i] : 0.0f, s);
+          bad |= !(fabsf(a[u][i]) <= kFloatMax);
+          m = fmaxf(m, fabsf(a[u][i]));
+        }
       }
     }
     s = warp_sum(s);
@@ -238,9 +246,9 @@ struct MoeRun {
 // barrier, where they become
 //   kDown = false: inner = act(G) U of the run's rows and pairs, and their maximum;
 //   kDown = true:  the experts' outputs.
-template <int NT, int MODE, bool kDown>
+template <int NT, int S, int MODE, bool kDown>
 __global__ void __launch_bounds__(kMoeThreads, 2) moe_expert_kernel(const MoeArgs p) {
-  constexpr int S = few_steps(NT), kMats = kDown ? 1 : 2;
+  constexpr int kMats = kDown ? 1 : 2;
   constexpr int kAhead = kMoeRingBytes / 1024 / S;
   constexpr int kCols = 8 * NT;
   constexpr int kRunTiles = kMoeSumBytes / (kMats * 16 * kCols * 4);
@@ -357,7 +365,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_expert_kernel(const MoeArg
       for (int i = wr; i < run.tiles; i += WR)
 #pragma unroll 1
         for (int m = 0; m < kMats; ++m) {
-          int acc[planes(MODE)][NT][4];
+          int acc[4][NT][4];
           ternary_clear<NT, MODE>(acc, minus);
           cp_async_wait<kAhead - 1>();
 #pragma unroll
