@@ -1339,8 +1339,8 @@ bl_status launch_moe_expert_s(const bl::MoeArgs& a, int grid, cudaStream_t s) {
 }
 
 // Chooses how the warps of a block share K (wk of them, S steps each, in `passes` turns): the
-// shortest time of a warp, its turns over the tiles of its block times their steps, if every
-// expert that can have a token has one; of equals the fewest turns (each loads codes).
+// shortest time of a warp, its tiles times their steps, if every expert that can have a token
+// has one, and 3.5 steps for the loading of the codes of a turn (measured).
 template <int NT, int MODE, bool kDown>
 bl_status launch_moe_expert(bl::MoeArgs a, cudaStream_t s) {
   constexpr int kMost = bl::few_steps(NT);  // kMost or kMost - 1 steps a warp
@@ -1353,7 +1353,7 @@ bl_status launch_moe_expert(bl::MoeArgs a, cudaStream_t s) {
   for (int wk = 1; wk <= bl::kMoeWarps; wk *= 2)
     for (int n = kMost; n >= kMost - 1; --n) {
       const int passes = (steps + wk * n - 1) / (wk * n), rows = bl::kMoeWarps / wk;
-      const long long cost = ((mine + rows - 1) / rows * passes * n) * 64 + passes;
+      const long long cost = (mine + rows - 1) / rows * passes * n * 2 + 7 * passes;
       if (S == 0 || cost < best) {
         best = cost;
         S = n;
