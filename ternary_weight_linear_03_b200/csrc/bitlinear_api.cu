@@ -1212,36 +1212,68 @@ bl_status launch_few(const int8_t* xq, const float* scale, const uint8_t* packed
 struct NormPlan {
   int threads, V;
 };
-NormPlan norm_plan(int K) {
+// Forward. Up to one row per SM, latency counts: one vector per thread. Beyond, two, so that
+// several blocks per SM overlap their loads, barriers and stores (4096 x 8192 bf16, 1 / 2 / 4
+// vectors: 55.3 / 42.9 / 46.8 us); four for short fp32 rows (1021 x 3200: 6.7 -> 5.6 us), and as
+// many as two blocks per SM need for rows that 1024 threads do not hold so (1170 x 28672 bf16:
+// 61.7 -> 53.9 us).
+NormPlan norm_plan(int M, int K, bool bf16) {
   const int nv = K / 8;
   NormPlan p{};
-  p.V = nv <= 512 ? 1 : nv <= 1024 ? 2 : 4;
+  if (nv > 2 * bl::kNormMaxThreads) p.V = bf16 ? 8 : 4;
+  else if (M <= num_sms() && nv <= bl::kNormMaxThreads) p.V = 1;
+  else p.V = (!bf16 && nv <= 512) ? 4 : 2;
   p.threads = ((nv + p.V - 1) / p.V + 31) / 32 * 32;
   return p;
 }
 
 bool norm_shape_ok(int M, int K) { return shape_ok(M, 1, K) && K <= bl::kNormMaxK; }
 
-template <bool kBf16>
-bl_status launch_rmsnorm(const void* x, const void* r, const void* w, int w_bf16, float eps, int M,
-                         int K, void* h, void* normed, int8_t* xq, float* scale, float* rstd,
-                         cudaStream_t s) {
-  const NormPlan p = norm_plan(K);
-  switch (p.V) {
-    case 1:
-      bl::rmsnorm_quant_kernel<kBf16, 1><<<M, p.threads, 0, s>>>(x, r, w, w_bf16, eps, K, h, normed, xq, scale, rstd);
-      break;
-    case 2:
-      bl::rmsnorm_quant_kernel<kBf16, 2><<<M, p.threads, 0, s>>>(x, r, w, w_bf16, eps, K, h, normed, xq, scale, rstd);
-      break;
-    default:
-      bl::rmsnorm_quant_kernel<kBf16, 4><<<M, p.threads, 0, s>>>(x, r, w, w_bf16, eps, K, h, normed, xq, scale, rstd);
-  }
-  return launch_status();
+struct NormArgs {
+  const void *x, *r, *w;
+  float eps;
+  int M, K;
+  void *h, *normed;
+  int8_t* xq;
+  float *scale, *rstd;
+};
+
+template <bool kBf16, bool kWBf16, int V>
+bl_status launch_rmsnorm_v(const NormArgs& a, int threads, cudaStream_t s) {
+  return launch_ex(bl::rmsnorm_quant_kernel<kBf16, kWBf16, V>, dim3(a.M), dim3(threads), 0, s, false, a.x, a.r,
+                   a.w, a.eps, a.K, a.h, a.normed, a.xq, a.scale, a.rstd);
 }
 
-// Blocks of the gradient kernel (each leaves one row of partial sums of grad_w).
-int norm_backward_blocks(int M) { return std::min(M, 2 * num_sms()); }
+template <bool kBf16, bool kWBf16>
+bl_status launch_rmsnorm(const NormArgs& a, cudaStream_t s) {
+  const NormPlan p = norm_plan(a.M, a.K, kBf16);
+  if (p.V == 1) return launch_rmsnorm_v<kBf16, kWBf16, 1>(a, p.threads, s);
+  if (p.V == 2) return launch_rmsnorm_v<kBf16, kWBf16, 2>(a, p.threads, s);
+  return launch_rmsnorm_v<kBf16, kWBf16, kBf16 ? 8 : 4>(a, p.threads, s);
+}
+
+// Gradient: as few blocks per row (cs), and vectors per thread, as keep a block at 512 threads.
+struct NormBwdPlan {
+  int cs, V, threads;
+};
+NormBwdPlan norm_backward_plan(int K) {
+  const int nv = K / 8;
+  NormBwdPlan p{};
+  for (p.cs = 1; nv > p.cs * bl::kNormBwdMaxV * bl::kNormBwdThreads; p.cs *= 2) {
+  }
+  const int each = (nv + p.cs - 1) / p.cs;
+  p.V = each <= bl::kNormBwdThreads ? 1 : 2;
+  p.threads = ((each + p.V - 1) / p.V + 31) / 32 * 32;
+  return p;
+}
+// Rows taken side by side (each leaves one row of partial sums of grad_w): as many as are
+// resident.
+int norm_backward_rows(int M, int K) {
+  const NormBwdPlan p = norm_backward_plan(K);
+  const int per_sm = std::max(1, bl::kNormBwdThreads / p.threads);
+  // clusters of four 512-thread blocks leave 16 of the 148 SMs out
+  return std::min(M, p.cs == 1 ? num_sms() * per_sm : num_sms() * (p.cs == 2 ? 74 : 33) / 148);
+}
 
 struct NormBwdArgs {
   const void *g, *h, *w;
@@ -1253,29 +1285,41 @@ struct NormBwdArgs {
   int M, K;
 };
 
-template <bool H, bool G, bool O, int V, bool R>
-bl_status launch_norm_backward_t(const NormBwdArgs& a, int threads, cudaStream_t s) {
-  const int blocks = norm_backward_blocks(a.M);
-  bl::rmsnorm_backward_kernel<H, G, O, V, R><<<blocks, threads, 0, s>>>(
-      a.g, a.h, a.w, a.w_bf16, a.rstd, a.grad_h, a.grad_x, a.part, a.M, a.K);
-  if (launch_status() != BL_OK) return BL_ERR_CUDA;
-  bl::rmsnorm_grad_weight_kernel<<<a.K / 32, bl::kNormGwThreads, 0, s>>>(a.part, blocks, a.K, a.grad_w);
-  return launch_status();
+template <bool H, bool G, bool O, bool W, int V>
+bl_status launch_norm_backward_t(const NormBwdArgs& a, const NormBwdPlan& p, cudaStream_t s) {
+  const int rows = norm_backward_rows(a.M, a.K);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(rows * p.cs);
+  cfg.blockDim = dim3(p.threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.cs;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cs > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, bl::rmsnorm_backward_kernel<H, G, O, W, V>, a.g, a.h, a.w, a.rstd, a.grad_h,
+                         a.grad_x, a.part, a.M, a.K, p.cs) != cudaSuccess)
+    return BL_ERR_CUDA;
+  return launch_ex(bl::rmsnorm_grad_weight_kernel, dim3(a.K / 32), dim3(bl::kNormGwThreads), 0, s, true,
+                   static_cast<const float*>(a.part), rows, a.K, a.grad_w);
+}
+
+template <bool H, bool G, bool O, bool W>
+bl_status launch_norm_backward_v(const NormBwdArgs& a, cudaStream_t s) {
+  const NormBwdPlan p = norm_backward_plan(a.K);
+  return p.V == 1 ? launch_norm_backward_t<H, G, O, W, 1>(a, p, s) : launch_norm_backward_t<H, G, O, W, 2>(a, p, s);
 }
 
 template <bool H, bool G, bool O>
-bl_status launch_norm_backward_v(const NormBwdArgs& a, cudaStream_t s) {
-  const NormPlan p = norm_plan(a.K);
-  if (p.V == 1) return launch_norm_backward_t<H, G, O, 1, false>(a, p.threads, s);
-  if (p.V == 2) return launch_norm_backward_t<H, G, O, 2, false>(a, p.threads, s);
-  if (p.threads <= bl::kNormMaxThreads / 2) return launch_norm_backward_t<H, G, O, 4, false>(a, p.threads, s);
-  return launch_norm_backward_t<H, G, O, 4, true>(a, p.threads, s);
+bl_status launch_norm_backward_w(const NormBwdArgs& a, cudaStream_t s) {
+  return a.w_bf16 ? launch_norm_backward_v<H, G, O, true>(a, s) : launch_norm_backward_v<H, G, O, false>(a, s);
 }
 
 template <bool H>
 bl_status launch_norm_backward_h(const NormBwdArgs& a, bool g_bf16, bool o_bf16, cudaStream_t s) {
-  if (g_bf16) return o_bf16 ? launch_norm_backward_v<H, true, true>(a, s) : launch_norm_backward_v<H, true, false>(a, s);
-  return o_bf16 ? launch_norm_backward_v<H, false, true>(a, s) : launch_norm_backward_v<H, false, false>(a, s);
+  if (g_bf16) return o_bf16 ? launch_norm_backward_w<H, true, true>(a, s) : launch_norm_backward_w<H, true, false>(a, s);
+  return o_bf16 ? launch_norm_backward_w<H, false, true>(a, s) : launch_norm_backward_w<H, false, false>(a, s);
 }
 
 bool float_dtype(int d) { return d == BL_F32 || d == BL_BF16; }
@@ -1415,15 +1459,15 @@ bl_status bitlinear_rmsnorm_quantize(const void* x, const void* residual, int x_
       !aligned16(normed) || !aligned16(xq) || !aligned16(scale) || !aligned16(rstd))
     return BL_ERR_MISALIGNED;  // a null pointer is aligned
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int wb = w_dtype == BL_BF16 ? 1 : 0;
-  return x_dtype == BL_BF16
-             ? launch_rmsnorm<true>(x, residual, weight, wb, eps, M, K, h, normed, xq, scale, rstd, s)
-             : launch_rmsnorm<false>(x, residual, weight, wb, eps, M, K, h, normed, xq, scale, rstd, s);
+  const NormArgs a{x, residual, weight, eps, M, K, h, normed, xq, scale, rstd};
+  if (x_dtype == BL_BF16)
+    return w_dtype == BL_BF16 ? launch_rmsnorm<true, true>(a, s) : launch_rmsnorm<true, false>(a, s);
+  return w_dtype == BL_BF16 ? launch_rmsnorm<false, true>(a, s) : launch_rmsnorm<false, false>(a, s);
 }
 
 size_t bitlinear_rmsnorm_backward_workspace_size(int M, int K) {
   if (!norm_shape_ok(M, K)) return 0;
-  return align_up(static_cast<size_t>(norm_backward_blocks(M)) * K * 4, 256);
+  return align_up(static_cast<size_t>(norm_backward_rows(M, K)) * K * 4, 256);
 }
 
 bl_status bitlinear_rmsnorm_backward(const void* grad_n, int gn_dtype, const void* h, int h_dtype,

@@ -137,15 +137,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
 // The 16 bytes at shared address `addr` of this block, in block `rank` of the cluster.
 __device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr, uint32_t rank) {
   uint32_t a;

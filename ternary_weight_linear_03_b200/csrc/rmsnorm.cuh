@@ -17,14 +17,63 @@
 namespace bl {
 
 constexpr float kFloatMax = 3.4028234663852886e38f;
-constexpr int kNormMaxV = 4;                              // 8-element vectors per thread, at most
 constexpr int kNormMaxThreads = 1024;
-constexpr int kNormMaxK = kNormMaxThreads * kNormMaxV * 8;  // a row is held by one block
+constexpr int kNormMaxK = kNormMaxThreads * 4 * 8;  // a row is held by one block
 
-// Rounds to the storage type and back.
+// 8 elements as they are stored.
 template <bool kBf16>
-__device__ __forceinline__ float round_to(float v) {
-  return kBf16 ? __bfloat162float(__float2bfloat16_rn(v)) : v;
+struct Raw8 {
+  uint4 v[kBf16 ? 1 : 2];
+};
+template <bool kBf16>
+__device__ __forceinline__ Raw8<kBf16> load_raw8(const void* row, int c) {
+  Raw8<kBf16> r;
+#pragma unroll
+  for (int i = 0; i < (kBf16 ? 1 : 2); ++i) r.v[i] = reinterpret_cast<const uint4*>(row)[(kBf16 ? 1 : 2) * c + i];
+  return r;
+}
+template <bool kBf16>
+__device__ __forceinline__ void store_raw8(void* row, int c, const Raw8<kBf16>& r) {
+#pragma unroll
+  for (int i = 0; i < (kBf16 ? 1 : 2); ++i) reinterpret_cast<uint4*>(row)[(kBf16 ? 1 : 2) * c + i] = r.v[i];
+}
+template <bool kBf16>
+__device__ __forceinline__ void unpack8(const Raw8<kBf16>& r, float (&v)[8]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (kBf16) {
+      const uint32_t h = q == 0 ? r.v[0].x : q == 1 ? r.v[0].y : q == 2 ? r.v[0].z : r.v[0].w;
+      v[2 * q] = __uint_as_float(h << 16);
+      v[2 * q + 1] = __uint_as_float(h & 0xffff0000u);
+    } else {
+      const uint4& u = r.v[q >> 1];
+      v[2 * q] = __uint_as_float((q & 1) ? u.z : u.x);
+      v[2 * q + 1] = __uint_as_float((q & 1) ? u.w : u.y);
+    }
+  }
+}
+// The sum of two, rounded to the storage type.
+template <bool kBf16>
+__device__ __forceinline__ Raw8<kBf16> add_raw8(const Raw8<kBf16>& a, const Raw8<kBf16>& b) {
+  float x[8], y[8];
+  unpack8<kBf16>(a, x);
+  unpack8<kBf16>(b, y);
+  uint32_t w[kBf16 ? 4 : 8];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float u = __fadd_rn(x[2 * q], y[2 * q]), v = __fadd_rn(x[2 * q + 1], y[2 * q + 1]);
+    if constexpr (kBf16) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(u, v);
+      w[q] = *reinterpret_cast<const uint32_t*>(&p);
+    } else {
+      w[2 * q] = __float_as_uint(u);
+      w[2 * q + 1] = __float_as_uint(v);
+    }
+  }
+  Raw8<kBf16> r;
+#pragma unroll
+  for (int i = 0; i < (kBf16 ? 1 : 2); ++i) r.v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  return r;
 }
 
 template <bool kBf16>
@@ -43,10 +92,6 @@ __device__ __forceinline__ void store8(void* row, int c, const float (&v)[8]) {
   }
 }
 
-__device__ __forceinline__ void load8_any(const void* row, bool bf16, int c, float (&v)[8]) {
-  if (bf16) load8<true>(row, c, v); else load8<false>(row, c, v);
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -57,40 +102,47 @@ __device__ __forceinline__ size_t row_offset(int t, int K, bool bf16) {
   return static_cast<size_t>(t) * static_cast<size_t>(K) * (bf16 ? 2 : 4);
 }
 
-// One block per row; thread i holds vectors i, i + blockDim.x, ... (V at most) of 8 elements.
+// One block per row; thread i holds vectors i, i + blockDim.x, ... (V at most) of 8 elements, as
+// stored (p is formed again from them for the codes: half the registers, twice the blocks).
 // r, h, normed and rstd_out may be null; h may be x's or r's own memory (each thread reads its
 // elements before it writes them).
-template <bool kBf16, int V>
+template <bool kBf16, bool kWBf16, int V>
 __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_quant_kernel(
-    const void* x, const void* r, const void* __restrict__ w, int w_bf16, float eps, int K,
+    const void* x, const void* r, const void* __restrict__ w, float eps, int K,
     void* h, void* normed, int8_t* __restrict__ xq, float* __restrict__ scale,
     float* __restrict__ rstd_out) {
   __shared__ float red_s[32], red_m[32];
+  allow_dependent_launch();  // a kernel that waits for this one may set itself up meanwhile
   const int t = blockIdx.x, T = blockDim.x, nv = K / 8;
   const size_t off = row_offset(t, K, kBf16);
   const char* xr = static_cast<const char*>(x) + off;
   const char* rr = r ? static_cast<const char*>(r) + off : nullptr;
-  float p[V][8];
+  Raw8<kBf16> hv[V];
   float ss = 0.0f, m = 0.0f;
+  // every load of the row before the first use
+#pragma unroll
+  for (int v = 0; v < V; ++v) hv[v] = load_raw8<kBf16>(xr, min(v * T + static_cast<int>(threadIdx.x), nv - 1));
+  if (rr) {
+    Raw8<kBf16> b[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) b[v] = load_raw8<kBf16>(rr, min(v * T + static_cast<int>(threadIdx.x), nv - 1));
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      hv[v] = add_raw8<kBf16>(hv[v], b[v]);
+      if (h && v * T + threadIdx.x < nv) store_raw8<kBf16>(static_cast<char*>(h) + off, v * T + threadIdx.x, hv[v]);
+    }
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = v * T + threadIdx.x;
     if (c < nv) {
-      load8<kBf16>(xr, c, p[v]);
-      if (rr) {
-        float b[8];
-        load8<kBf16>(rr, c, b);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[v][i] = round_to<kBf16>(__fadd_rn(p[v][i], b[i]));
-        if (h) store8<kBf16>(static_cast<char*>(h) + off, c, p[v]);
-      }
-      float g[8];
-      load8_any(w, w_bf16, c, g);
+      float p[8], g[8];
+      unpack8<kBf16>(hv[v], p);
+      load8<kWBf16>(w, c, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        ss = fmaf(p[v][i], p[v][i], ss);
-        p[v][i] = __fmul_rn(p[v][i], g[i]);
-        m = fmaxf(m, fabsf(p[v][i]));
+        ss = fmaf(p[i], p[i], ss);
+        m = fmaxf(m, fabsf(__fmul_rn(p[i], g[i])));
       }
     }
   }
@@ -118,15 +170,20 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_quant_kernel(
   for (int v = 0; v < V; ++v) {
     const int c = v * T + threadIdx.x;
     if (c < nv) {
+      float p[8], g[8];
+      unpack8<kBf16>(hv[v], p);
+      load8<kWBf16>(w, c, g);
       uint32_t q[2] = {0u, 0u};
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        q[i >> 2] |= (static_cast<uint32_t>(quant_i8(p[v][i], f)) & 0xffu) << (8 * (i & 3));
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __fmul_rn(p[i], g[i]);
+        q[i >> 2] |= (static_cast<uint32_t>(quant_i8(p[i], f)) & 0xffu) << (8 * (i & 3));
+      }
       reinterpret_cast<uint2*>(qrow)[c] = make_uint2(q[0], q[1]);
       if (normed) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[v][i] = __fmul_rn(p[v][i], rstd);
-        store8<kBf16>(static_cast<char*>(normed) + off, c, p[v]);
+        for (int i = 0; i < 8; ++i) p[i] = __fmul_rn(p[i], rstd);
+        store8<kBf16>(static_cast<char*>(normed) + off, c, p);
       }
     }
   }
@@ -135,100 +192,135 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_quant_kernel(
 // Gradient. With hat = h rstd and d = g w (g the gradient of the norm's output; the
 // quantizer passes it straight through):
 //   grad_x = grad_h + rstd (d - hat mean_k(d hat)),   grad_w[k] = sum_t g[t,k] hat[t,k]
-// grad_x belongs to x and to the residual alike. Block b takes rows b, b + gridDim.x, ...;
-// a thread keeps the same columns for all of them, so its part of grad_w stays in
-// registers and is written once, to row b of part (summed over b by
-// rmsnorm_grad_weight_kernel in a fixed order: no atomics, the same bits every time).
-// Rows of more than 512 x V vectors leave 64 registers a thread: kReload reads h and g again
-// (from L1/L2) for the second half instead of keeping them.
-template <bool kHBf16, bool kGBf16, bool kOBf16, int V, bool kReload>
-__global__ void __launch_bounds__(kReload ? kNormMaxThreads : kNormMaxThreads / 2) rmsnorm_backward_kernel(
-    const void* __restrict__ g, const void* __restrict__ h, const void* __restrict__ w, int w_bf16,
+// grad_x belongs to x and to the residual alike. Block b takes rows b, b + gridDim.x, ...; a
+// thread keeps the same columns for all of them, so its part of grad_w stays in registers and is
+// written once, to row b of part (summed over b by rmsnorm_grad_weight_kernel in a fixed
+// order: no atomics, the same bits every time). Bound by memory: the next row's h and g are on
+// their way while a row is reduced and written (one block of 512 threads fills an SM's
+// registers, so nothing else would be; 4096 x 8192: 105 -> 58 us). Rows of more than 8192 are
+// split over a cluster of cs blocks, which exchange their part of the row's sum.
+constexpr int kNormBwdThreads = 512;
+constexpr int kNormBwdMaxV = 2;
+template <bool kHBf16, bool kGBf16, bool kOBf16, bool kWBf16, int V>
+__global__ void __launch_bounds__(kNormBwdThreads) rmsnorm_backward_kernel(
+    const void* __restrict__ g, const void* __restrict__ h, const void* __restrict__ w,
     const float* __restrict__ rstd, const void* grad_h, void* grad_x, float* __restrict__ part,
-    int M, int K) {
-  __shared__ float red[32];
-  const int T = blockDim.x, nv = K / 8;
+    int M, int K, int cs) {
+  __shared__ float red[2][32];
+  __shared__ float sum[2];
+  const int T = blockDim.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = T >> 5;
+  const int rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
+  // vectors of 8 columns [nv0, nv1) of this block
+  const int each = (K / 8 + cs - 1) / cs, nv0 = min(rank * each, K / 8), nv1 = min(nv0 + each, K / 8);
+  const int first = blockIdx.x / cs, stride = gridDim.x / cs;
   float dw[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[v][i] = 0.0f;
-  for (int t = blockIdx.x; t < M; t += gridDim.x) {
-    const char* hr = static_cast<const char*>(h) + row_offset(t, K, kHBf16);
-    const char* gr = static_cast<const char*>(g) + row_offset(t, K, kGBf16);
-    const size_t oo = row_offset(t, K, kOBf16);
-    const float rs = rstd[t];
-    constexpr int kKeep = kReload ? 1 : V;
-    float hat[kKeep][8], d[kKeep][8];
-    float dot = 0.0f;
-    auto take = [&](int c, float (&ht)[8], float (&dv)[8], bool first, float (&sum)[8]) {
-      float wv[8];
-      load8<kHBf16>(hr, c, ht);
-      load8<kGBf16>(gr, c, dv);
-      load8_any(w, w_bf16, c, wv);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ht[i] = __fmul_rn(ht[i], rs);
-        if (first) sum[i] = fmaf(dv[i], ht[i], sum[i]);
-        dv[i] = __fmul_rn(dv[i], wv[i]);
-        if (first) dot = fmaf(dv[i], ht[i], dot);
-      }
-    };
+  auto at = [&](int v) { return nv0 + v * T + static_cast<int>(threadIdx.x); };
+  auto column = [&](int v) { return max(min(at(v), nv1 - 1), 0); };
+  Raw8<kHBf16> hn[V];
+  Raw8<kGBf16> gn[V];
+  auto fetch = [&](int t) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = v * T + threadIdx.x, i = kReload ? 0 : v;
-      if (c < nv) take(c, hat[i], d[i], true, dw[v]);
+      hn[v] = load_raw8<kHBf16>(static_cast<const char*>(h) + row_offset(t, K, kHBf16), column(v));
+      gn[v] = load_raw8<kGBf16>(static_cast<const char*>(g) + row_offset(t, K, kGBf16), column(v));
+    }
+  };
+  // hat, g and d of a vector
+  auto values = [&](const Raw8<kHBf16>& hr, const Raw8<kGBf16>& gr, float rs, int v, float (&hat)[8],
+                    float (&gv)[8], float (&d)[8]) {
+    float wv[8];
+    unpack8<kHBf16>(hr, hat);
+    unpack8<kGBf16>(gr, gv);
+    load8<kWBf16>(w, column(v), wv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hat[i] = __fmul_rn(hat[i], rs);
+      d[i] = __fmul_rn(gv[i], wv[i]);
+    }
+  };
+  fetch(first);
+  int turn = 0;
+  for (int t = first; t < M; t += stride, turn ^= 1) {
+    const size_t oo = row_offset(t, K, kOBf16);
+    const float rs = rstd[t];
+    Raw8<kHBf16> hc[V];
+    Raw8<kGBf16> gc[V];
+    Raw8<kOBf16> past[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      hc[v] = hn[v];
+      gc[v] = gn[v];
+      if (grad_h) past[v] = load_raw8<kOBf16>(static_cast<const char*>(grad_h) + oo, column(v));
+    }
+    fetch(min(t + stride, M - 1));
+    float dot = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float hat[8], gv[8], d[8];
+      values(hc[v], gc[v], rs, v, hat, gv, d);
+      if (at(v) < nv1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dw[v][i] = fmaf(gv[i], hat[i], dw[v][i]);
+          dot = fmaf(d[i], hat[i], dot);
+        }
+      }
     }
     dot = warp_sum(dot);
-    if (lane == 0) red[warp] = dot;
+    if (lane == 0) red[turn][warp] = dot;
     __syncthreads();
-    dot = warp_sum(lane < warps ? red[lane] : 0.0f);
-    __syncthreads();  // red is written again for the next row
+    dot = warp_sum(lane < warps ? red[turn][lane] : 0.0f);
+    if (cs > 1) {
+      if (threadIdx.x == 0) sum[turn] = dot;
+      cluster_barrier();
+      dot = 0.0f;
+      for (int k = 0; k < cs; ++k) dot += ld_cluster_f32(smem_u32(&sum[turn]), k);
+    }
     const float mean = __fdiv_rn(dot, static_cast<float>(K));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = v * T + threadIdx.x, iv = kReload ? 0 : v;
-      if (c < nv) {
-        float o[8];
-        if (kReload) take(c, hat[0], d[0], false, dw[v]);
+      if (at(v) < nv1) {
+        float hat[8], gv[8], d[8], o[8];
+        values(hc[v], gc[v], rs, v, hat, gv, d);
         if (grad_h) {
-          load8<kOBf16>(static_cast<const char*>(grad_h) + oo, c, o);
+          unpack8<kOBf16>(past[v], o);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = 0.0f;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          o[i] = fmaf(rs, fmaf(-hat[iv][i], mean, d[iv][i]), o[i]);
-        store8<kOBf16>(static_cast<char*>(grad_x) + oo, c, o);
+        for (int i = 0; i < 8; ++i) o[i] = fmaf(rs, fmaf(-hat[i], mean, d[i]), o[i]);
+        store8<kOBf16>(static_cast<char*>(grad_x) + oo, at(v), o);
       }
     }
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = v * T + threadIdx.x;
-    if (c < nv) store8<false>(part + static_cast<size_t>(blockIdx.x) * K, c, dw[v]);
-  }
+  for (int v = 0; v < V; ++v)
+    if (at(v) < nv1) store8<false>(part + static_cast<size_t>(first) * K, at(v), dw[v]);
+  if (cs > 1) cluster_barrier();  // no block leaves while others read its sum
 }
 
-// grad_w[k] = sum_b part[b][k]. A block takes 32 columns; its 8 warps take rows b = w, w + 8,
+// grad_w[k] = sum_b part[b][k]. A block takes 32 columns; its 32 warps take rows b = w, w + 32,
 // ... and are added in order.
-constexpr int kNormGwThreads = 256;
+constexpr int kNormGwThreads = 1024;
 __global__ void __launch_bounds__(kNormGwThreads) rmsnorm_grad_weight_kernel(
     const float* __restrict__ part, int rows, int K, float* __restrict__ grad_w) {
-  __shared__ float red[8][32];
+  __shared__ float red[32][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int k = blockIdx.x * 32 + lane;  // K % 64 == 0: always inside
   float s = 0.0f;
-  for (int b = warp; b < rows; b += 8) s += part[static_cast<size_t>(b) * K + k];
+  grid_dependency_wait();
+#pragma unroll 8
+  for (int b = warp; b < rows; b += 32) s += part[static_cast<size_t>(b) * K + k];
   red[warp][lane] = s;
   __syncthreads();
-  if (warp == 0) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][lane];
-    grad_w[k] = s;
-  }
+  s = warp_sum(red[lane][warp]);
+  if (lane == 0) grad_w[blockIdx.x * 32 + warp] = s;
 }
 
 }  // namespace bl
