@@ -161,32 +161,55 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
-def _run(fn, what: str, device: torch.device, stream, *args) -> None:
-    """Calls fn(*args, stream) with `device` current (on its current stream if none is given)."""
-    at = device.index
-    if at == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), what)
-        return
-    with torch.cuda.device(at):
-        _check(fn(*args, _stream(stream)), what)
+# The current stream's handle without a Stream object (3 us less per call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _take(t: torch.Tensor, name: str, shape, dtype, device: torch.device) -> int:
-    """Address of a contiguous tensor of this shape and type (one of them) on this device."""
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+def _run(fn, what: str, at: int, stream, *args) -> None:
+    """Calls fn(*args, stream) with device `at` current (on its current stream if none is given)."""
+    if at != torch.cuda.current_device():
+        with torch.cuda.device(at):
+            return _run(fn, what, at, stream, *args)
+    if stream is None:
+        handle = _raw_stream(at) if _raw_stream is not None else _stream(None)
+    else:
+        handle = stream.cuda_stream
+    status = fn(*args, handle)
+    if status:
+        _check(status, what)
+
+
+def _take(t: torch.Tensor, name: str, shape, dtype, at: int) -> int:
+    """Address of a contiguous tensor of this shape and type (one of them) on device `at`."""
+    if t.get_device() != at:
+        raise ValueError(f"{name} must be on cuda:{at}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.dtype not in dtype if isinstance(dtype, tuple) else t.dtype != dtype:
+    if t.dtype is not dtype and (dtype is not _FLOATS or t.dtype not in _FLOATS):
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    return _dev(t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _take_ws(ws: torch.Tensor, at: int) -> int:
+    if ws.get_device() != at or not ws.is_contiguous() or ws.dtype is not torch.uint8:
+        raise ValueError(f"ws must be a contiguous uint8 tensor on cuda:{at}")
+    return ws.data_ptr()
+
+
+def _index(t: torch.Tensor, name: str) -> int:
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return at
 
 
 _FLOATS = (torch.float32, torch.bfloat16)
 
 
-def _take_or_none(t, name, shape, dtype, device):
-    return None if t is None else _take(t, name, shape, dtype, device)
+def _code(t: torch.Tensor) -> int:
+    return BL_BF16 if t.dtype is torch.bfloat16 else BL_F32
 
 
 def workspace_size(M: int, N: int, K: int) -> int:
@@ -426,20 +449,18 @@ def backward_quantized(xq: torch.Tensor, scale: torch.Tensor, grad_y: torch.Tens
                        packedT: torch.Tensor, gamma: torch.Tensor, need_x: bool = True,
                        need_w: bool = True, ws: torch.Tensor | None = None, stream=None):
     """backward for a forward that ran on int8 activations xq [M][K] with scales [M]."""
-    lib = load_library()
-    (M, K), N, dev = xq.shape, grad_y.shape[1], xq.device
-    gx = torch.empty((M, K), dtype=torch.float32, device=dev) if need_x else None
-    gw = torch.empty((N, K), dtype=torch.float32, device=dev) if need_w else None
+    (M, K), N, at = xq.shape, grad_y.shape[1], _index(xq, "xq")
+    gx = scale.new_empty((M, K)) if need_x else None
+    gw = scale.new_empty((N, K)) if need_w else None
     if ws is None and need_w:
-        ws = backward_workspace(M, N, K, dev)
-    _run(lib.bitlinear_backward_quantized, "bitlinear_backward_quantized", dev, stream,
-         _take(xq, "xq", (M, K), torch.int8, dev), _take(scale, "scale", (M,), torch.float32, dev),
-         _take(grad_y, "grad_y", (M, N), torch.bfloat16, dev),
-         _take(packedT, "packedT", (K, N // 4), torch.uint8, dev),
-         _take(gamma, "gamma", (1,), torch.float32, dev),
+        ws = backward_workspace(M, N, K, xq.device)
+    _run((_lib or load_library()).bitlinear_backward_quantized, "bitlinear_backward_quantized", at, stream,
+         _take(xq, "xq", (M, K), torch.int8, at), _take(scale, "scale", (M,), torch.float32, at),
+         _take(grad_y, "grad_y", (M, N), torch.bfloat16, at),
+         _take(packedT, "packedT", (K, N // 4), torch.uint8, at),
+         _take(gamma, "gamma", (1,), torch.float32, at),
          gx.data_ptr() if need_x else None, gw.data_ptr() if need_w else None, M, N, K,
-         None if ws is None else _take(ws, "ws", ws.shape, torch.uint8, dev),
-         0 if ws is None else ws.numel())
+         None if ws is None else _take_ws(ws, at), 0 if ws is None else ws.numel())
     return gx, gw
 
 
@@ -449,18 +470,16 @@ def forward_quantized(xq: torch.Tensor, scale: torch.Tensor, packed: torch.Tenso
                       stream=None) -> torch.Tensor:
     """BitLinear forward of int8 activations xq [M][K] with scales [M] (rmsnorm_quantize,
     quantize_acts): y [M][N]."""
-    lib = load_library()
-    (M, K), N, dev = xq.shape, packed.shape[0], xq.device
+    (M, K), N, at = xq.shape, packed.shape[0], _index(xq, "xq")
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=dev)
+        y = xq.new_empty((M, N), dtype=out_dtype)
     if ws is None and (M > FEW_TOKENS or K > 32768):
-        ws = workspace(M, N, K, dev)
-    _run(lib.bitlinear_forward_quantized, "bitlinear_forward_quantized", dev, stream,
-         _take(xq, "xq", (M, K), torch.int8, dev), _take(scale, "scale", (M,), torch.float32, dev),
-         _take(packed, "packed", (N, K // 4), torch.uint8, dev),
-         _take(gamma, "gamma", (1,), torch.float32, dev), _take(y, "y", (M, N), _FLOATS, dev),
-         _dtype_code(y), M, N, K, None if ws is None else _take(ws, "ws", ws.shape, torch.uint8, dev),
-         0 if ws is None else ws.numel())
+        ws = workspace(M, N, K, xq.device)
+    _run((_lib or load_library()).bitlinear_forward_quantized, "bitlinear_forward_quantized", at, stream,
+         _take(xq, "xq", (M, K), torch.int8, at), _take(scale, "scale", (M,), torch.float32, at),
+         _take(packed, "packed", (N, K // 4), torch.uint8, at),
+         _take(gamma, "gamma", (1,), torch.float32, at), _take(y, "y", (M, N), _FLOATS, at),
+         _code(y), M, N, K, None if ws is None else _take_ws(ws, at), 0 if ws is None else ws.numel())
     return y
 
 
@@ -475,24 +494,26 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
     """RMS norm of h = x + residual with gain weight [K], as int8 codes: (xq [M][K], scale [M],
     h [M][K], rstd [M]). h is x itself without a residual; it may be given as x or residual
     (added in place). normed, if given, receives the normalised rows themselves."""
-    lib = load_library()
-    (M, K), dev, dt = x.shape, x.device, x.dtype
+    (M, K), at, dt = x.shape, _index(x, "x"), x.dtype
     if residual is None:
         h = x
     elif h is None:
-        h = torch.empty_like(x, memory_format=torch.contiguous_format)
+        h = x.new_empty((M, K))
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=dev)
+        xq = x.new_empty((M, K), dtype=torch.int8)
     if scale is None:
-        scale = torch.empty(M, dtype=torch.float32, device=dev)
+        scale = x.new_empty(M, dtype=torch.float32)
     if rstd is None:
-        rstd = torch.empty(M, dtype=torch.float32, device=dev)
-    _run(lib.bitlinear_rmsnorm_quantize, "bitlinear_rmsnorm_quantize", dev, stream,
-         _dev(x, "x"), _take_or_none(residual, "residual", (M, K), dt, dev), _dtype_code(x),
-         _take(weight, "weight", (K,), _FLOATS, dev), _dtype_code(weight), float(eps), M, K,
-         None if residual is None else _take(h, "h", (M, K), dt, dev),
-         _take_or_none(normed, "normed", (M, K), dt, dev), _take(xq, "xq", (M, K), torch.int8, dev),
-         _take(scale, "scale", (M,), torch.float32, dev), _take(rstd, "rstd", (M,), torch.float32, dev))
+        rstd = x.new_empty(M, dtype=torch.float32)
+    row = (M,)
+    _run((_lib or load_library()).bitlinear_rmsnorm_quantize, "bitlinear_rmsnorm_quantize", at, stream,
+         _take(x, "x", (M, K), _FLOATS, at),
+         None if residual is None else _take(residual, "residual", (M, K), dt, at), _code(x),
+         _take(weight, "weight", (K,), _FLOATS, at), _code(weight), eps, M, K,
+         None if residual is None else _take(h, "h", (M, K), dt, at),
+         None if normed is None else _take(normed, "normed", (M, K), dt, at),
+         _take(xq, "xq", (M, K), torch.int8, at), _take(scale, "scale", row, torch.float32, at),
+         _take(rstd, "rstd", row, torch.float32, at))
     return xq, scale, h, rstd
 
 
@@ -515,22 +536,20 @@ def rmsnorm_backward(grad_n: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
     the residual alike, grad_weight fp32 [K]) from the gradient grad_n of the normalised rows
     and, if given, the gradient grad_h that reaches h past the norm (of grad_x's type; grad_x
     may be grad_h itself)."""
-    lib = load_library()
-    (M, K), dev = h.shape, h.device
+    (M, K), at = h.shape, _index(h, "h")
     if grad_x is None:
-        grad_x = torch.empty((M, K), dtype=out_dtype, device=dev)
+        grad_x = h.new_empty((M, K), dtype=out_dtype)
     if grad_weight is None:
-        grad_weight = torch.empty(K, dtype=torch.float32, device=dev)
+        grad_weight = h.new_empty(K, dtype=torch.float32)
     if ws is None:
-        ws = rmsnorm_backward_workspace(M, K, dev)
-    _run(lib.bitlinear_rmsnorm_backward, "bitlinear_rmsnorm_backward", dev, stream,
-         _take(grad_n, "grad_n", (M, K), _FLOATS, dev), _dtype_code(grad_n), _dev(h, "h"),
-         _dtype_code(h), _take(weight, "weight", (K,), _FLOATS, dev), _dtype_code(weight),
-         _take(rstd, "rstd", (M,), torch.float32, dev),
-         _take_or_none(grad_h, "grad_h", (M, K), grad_x.dtype, dev),
-         _take(grad_x, "grad_x", (M, K), _FLOATS, dev), _dtype_code(grad_x),
-         _take(grad_weight, "grad_weight", (K,), torch.float32, dev), M, K,
-         _take(ws, "ws", ws.shape, torch.uint8, dev), ws.numel())
+        ws = rmsnorm_backward_workspace(M, K, h.device)
+    _run((_lib or load_library()).bitlinear_rmsnorm_backward, "bitlinear_rmsnorm_backward", at, stream,
+         _take(grad_n, "grad_n", (M, K), _FLOATS, at), _code(grad_n), _take(h, "h", (M, K), _FLOATS, at),
+         _code(h), _take(weight, "weight", (K,), _FLOATS, at), _code(weight),
+         _take(rstd, "rstd", (M,), torch.float32, at),
+         None if grad_h is None else _take(grad_h, "grad_h", (M, K), grad_x.dtype, at),
+         _take(grad_x, "grad_x", (M, K), _FLOATS, at), _code(grad_x),
+         _take(grad_weight, "grad_weight", (K,), torch.float32, at), M, K, _take_ws(ws, at), ws.numel())
     return grad_x, grad_weight
 
 
@@ -561,23 +580,24 @@ class MoeLayer:
                  renormalize: bool = True):
         if activation not in ACTIVATIONS:
             raise ValueError(f"activation must be one of {tuple(ACTIVATIONS)}")
-        (E, D), F, dev = router.shape, gate.shape[1], router.device
-        self.E, self.D, self.F, self.top_k, self.device = E, D, F, int(top_k), dev
+        (E, D), F, at = router.shape, gate.shape[1], _index(router, "router")
+        self.E, self.D, self.F, self.top_k, self.device = E, D, F, int(top_k), router.device
         self.tensors = (router, gate, up, down, gate_gamma, up_gamma, down_gamma)
         self.struct = Moe(
-            _take(router, "router", (E, D), _FLOATS, dev),
-            _take(gate, "gate", (E, F, D // 4), torch.uint8, dev),
-            _take(up, "up", (E, F, D // 4), torch.uint8, dev),
-            _take(down, "down", (E, D, F // 4), torch.uint8, dev),
-            _take(gate_gamma, "gate_gamma", (E,), torch.float32, dev),
-            _take(up_gamma, "up_gamma", (E,), torch.float32, dev),
-            _take(down_gamma, "down_gamma", (E,), torch.float32, dev),
-            _dtype_code(router), E, D, F, int(top_k), ACTIVATIONS[activation], int(bool(renormalize)))
+            _take(router, "router", (E, D), _FLOATS, at),
+            _take(gate, "gate", (E, F, D // 4), torch.uint8, at),
+            _take(up, "up", (E, F, D // 4), torch.uint8, at),
+            _take(down, "down", (E, D, F // 4), torch.uint8, at),
+            _take(gate_gamma, "gate_gamma", (E,), torch.float32, at),
+            _take(up_gamma, "up_gamma", (E,), torch.float32, at),
+            _take(down_gamma, "down_gamma", (E,), torch.float32, at),
+            _code(router), E, D, F, int(top_k), ACTIVATIONS[activation], int(bool(renormalize)))
+        self._ref = ctypes.byref(self.struct)
 
 
 def moe_workspace(M: int, layer: MoeLayer) -> torch.Tensor:
-    """A caller-owned device workspace for moe_forward of up to 64 tokens."""
-    n = int(load_library().bitlinear_moe_workspace_size(M, ctypes.byref(layer.struct)))
+    """A caller-owned device workspace for moe_forward of M tokens (or fewer)."""
+    n = int(load_library().bitlinear_moe_workspace_size(M, layer._ref))
     if n == 0:
         raise BitLinearError(2, "bitlinear_moe_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=layer.device)
@@ -587,16 +607,14 @@ def moe_forward(x: torch.Tensor, layer: MoeLayer, out_dtype: torch.dtype = torch
                 y: torch.Tensor | None = None, ws: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
     """A mixture-of-experts layer for a few tokens (up to 64): x [M][D] -> y [M][D]."""
-    lib = load_library()
-    M, dev = x.shape[0], layer.device
+    M, at, shape = x.shape[0], _index(layer.tensors[0], "router"), (x.shape[0], layer.D)
     if y is None:
-        y = torch.empty((M, layer.D), dtype=out_dtype, device=dev)
+        y = layer.tensors[0].new_empty(shape, dtype=out_dtype)
     if ws is None:
         ws = moe_workspace(M, layer)
-    _run(lib.bitlinear_moe_forward, "bitlinear_moe_forward", dev, stream,
-         _take(x, "x", (M, layer.D), _FLOATS, dev), _dtype_code(x), M, ctypes.byref(layer.struct),
-         _take(y, "y", (M, layer.D), _FLOATS, dev), _dtype_code(y),
-         _take(ws, "ws", ws.shape, torch.uint8, dev), ws.numel())
+    _run((_lib or load_library()).bitlinear_moe_forward, "bitlinear_moe_forward", at, stream,
+         _take(x, "x", shape, _FLOATS, at), _code(x), M, layer._ref, _take(y, "y", shape, _FLOATS, at), _code(y),
+         _take_ws(ws, at), ws.numel())
     return y
 
 
