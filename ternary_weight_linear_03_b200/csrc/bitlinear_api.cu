@@ -1344,7 +1344,6 @@ bl_status moe_check(int M, const bl_moe* m) {
 struct MoeWs {
   int8_t* xq;       // [M][D]
   float* scale;     // [M]
-  float* logits;    // [M][E]
   int* ids;         // [M * top_k]
   float* weights;   // [M * top_k]
   float* inner;     // [M * top_k][F]
@@ -1361,7 +1360,6 @@ MoeWs moe_ws_layout(void* base, int M, const bl_moe& m) {
   auto take = [&p](size_t bytes) { char* q = p; p += align_up(bytes, 256); return q; };
   w.xq = reinterpret_cast<int8_t*>(take(static_cast<size_t>(M) * m.D));
   w.scale = reinterpret_cast<float*>(take(M * 4));
-  w.logits = reinterpret_cast<float*>(take(static_cast<size_t>(M) * m.E * 4));
   w.ids = reinterpret_cast<int*>(take(P * 4));
   w.weights = reinterpret_cast<float*>(take(P * 4));
   w.inner = reinterpret_cast<float*>(take(P * m.F * 4));
@@ -1506,12 +1504,24 @@ bl_status bitlinear_moe_forward(const void* x, int x_dtype, int M, const bl_moe*
   const MoeWs w = moe_ws_layout(ws, M, m);
   const int n_clear = M * m.top_k;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid(M * bl::kRouteBlocks), block(bl::kRouteThreads);
+  const int blocks = 8 * M <= num_sms() ? 8 : 2;  // of a token: one wave of one block per SM
   int* clear = reinterpret_cast<int*>(w.amax);
   // launched in full order: the kernels of a call before may still use the workspace
   auto route = [&](auto kern) {
-    return launch_ex(kern, grid, block, 0, s, false, x, m.router, m.D, m.E, m.top_k, m.renormalize,
-                     w.logits, w.ids, w.weights, w.xq, w.scale, clear, n_clear);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(M * blocks);
+    cfg.blockDim = dim3(bl::kRouteThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, x, m.router, m.D, m.E, m.top_k, m.renormalize, w.ids, w.weights,
+                           w.xq, w.scale, clear, n_clear, blocks) != cudaSuccess)
+      return BL_ERR_CUDA;
+    return launch_status();
   };
   if (x_dtype == BL_BF16)
     st = m.router_dtype == BL_BF16 ? route(bl::moe_route_kernel<true, true>) : route(bl::moe_route_kernel<true, false>);

@@ -24,116 +24,112 @@ __device__ __forceinline__ float moe_act(float g, int act) {
 }
 
 // A float's bits as an unsigned number that orders like the float; NaN below everything.
-// Never 0.
 __device__ __forceinline__ uint32_t order_key(float v) {
   if (!(v == v)) return 1u;
   const uint32_t b = __float_as_uint(v);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// Top-k of a token's logits by one warp: lane l holds logits l, l + 32, ...
-__device__ __forceinline__ void moe_top_k(const float* logits, int E, int top_k, bool renorm,
-                                          int* __restrict__ ids, float* __restrict__ weights) {
-  constexpr int kPer = kMoeMaxExperts / 32;
-  const int lane = threadIdx.x & 31;
-  uint32_t key[kPer];
-  uint32_t best = 0u;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    key[i] = 0u;
-    if (32 * i >= E) continue;
-    const int e = 32 * i + lane;
-    const float v = e < E ? logits[e] : 0.0f;
-    bad |= !(fabsf(v) <= kFloatMax);
-    key[i] = e < E ? order_key(v) : 0u;
-    best = max(best, key[i]);
+// The choice among a token's E logits (shared memory) by a block of kThreads >= E threads, a
+// power of two: an expert's rank is the number of those before it, which as many lanes count as
+// there are threads for an expert (rounds of maxima, or one thread per expert, are chains of
+// thousands of cycles on a single warp). keys, chosen: shared memory for E and top_k words.
+template <int kThreads>
+__device__ __forceinline__ void moe_top_k(const float* logits, int E, int top_k, bool renorm, uint32_t* keys,
+                                          int* chosen, int* __restrict__ ids, float* __restrict__ weights) {
+  const int tid = threadIdx.x;
+  if (tid < E) {
+    const float mine = logits[tid];
+    if (!(fabsf(mine) <= kFloatMax)) record_status(kStatusNonfinite);
+    keys[tid] = order_key(mine);
   }
-  if (bad) record_status(kStatusNonfinite);
-  float top = 0.0f, sum = 0.0f, mine = 0.0f;
-  int mine_e = 0;
-  for (int s = 0; s < top_k; ++s) {
-    const uint32_t k = __reduce_max_sync(0xffffffffu, best);
-    uint32_t e = 0xffffffffu;
-#pragma unroll
-    for (int i = kPer - 1; i >= 0; --i)
-      if (32 * i < E && key[i] == k) e = 32 * i + lane;
-    e = __reduce_min_sync(0xffffffffu, e);
-    const float v = logits[e];
-    if (s == 0) top = v;
-    const float p = expf(v - top);
-    if (lane == s) { mine = p; mine_e = static_cast<int>(e); }
-    if (renorm) sum += p;
-    best = 0u;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (32 * i >= E) continue;
-      if (32u * i + lane == e) key[i] = 0u;
-      best = max(best, key[i]);
-    }
+  __syncthreads();
+  int share = 1;  // lanes to an expert
+  while (share < 32 && 2 * share * E <= kThreads) share *= 2;
+  const int e = tid / share;
+  int rank = 0;
+  if (e < E) {
+    const uint32_t key = keys[e];
+#pragma unroll 4
+    for (int i = tid % share; i < E; i += share) rank += keys[i] > key || (keys[i] == key && i < e);
   }
+  for (int o = 1; o < share; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+  if (e < E && tid % share == 0 && rank < top_k) chosen[rank] = e;
+  __syncthreads();
+  if (tid >= 32) return;
+  const float top = logits[chosen[0]];
+  const float mine = tid < top_k ? expf(logits[chosen[tid]] - top) : 0.0f;
+  float sum = mine;
   if (!renorm) {
-    for (int e = lane; e < E; e += 32) sum += expf(logits[e] - top);
-    sum = warp_sum(sum);
+    sum = 0.0f;
+    for (int i = tid; i < E; i += 32) sum += expf(logits[i] - top);
   }
-  if (lane < top_k) {
-    ids[lane] = mine_e;
-    weights[lane] = __fdiv_rn(mine, sum);
+  sum = warp_sum(sum);
+  if (tid < top_k) {
+    ids[tid] = chosen[tid];
+    weights[tid] = __fdiv_rn(mine, sum);
   }
 }
 
 // ------------------------------------------------------------------------------- route
-// One cluster of 8 blocks per token. Each block takes an eighth of the experts' logits and
-// quantizes an eighth of the row, and the first one chooses. Also clears what the next kernels
+// One cluster of `blocks` blocks (8, or 2 when there are more tokens than eighths of the GPU) per
+// token. Each block takes its share of the experts' logits and of the row's codes, and the
+// first one chooses. Also clears what the next kernels
 // add to. Bound by latency: as many warps share an expert's dot product as the block has, so
 // that all of the router is asked for at once (8 warps, one per expert, left most of its 512 KB
 // waiting: 64 experts of 4096, one token, 5.9 -> 3.6 us).
 constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kRouteBlocks = 8;
 
 template <bool kXBf16, bool kRBf16>
-__global__ void __launch_bounds__(kRouteThreads) __cluster_dims__(kRouteBlocks, 1, 1)
-moe_route_kernel(const void* __restrict__ x, const void* __restrict__ router, int D, int E,
-                 int top_k, int renorm, float* logits_all, int* __restrict__ ids,
+__global__ void __launch_bounds__(kRouteThreads, 1) moe_route_kernel(
+    const void* __restrict__ x, const void* __restrict__ router, int D, int E,
+                 int top_k, int renorm, int* __restrict__ ids,
                  float* __restrict__ weights, int8_t* __restrict__ xq, float* __restrict__ xscale,
-                 int* __restrict__ clear, int n_clear) {
-  __shared__ float logits[kMoeMaxExperts];
+                 int* __restrict__ clear, int n_clear, int blocks) {
+  __shared__ __align__(16) float logits[kMoeMaxExperts];
+  __shared__ uint32_t keys[kMoeMaxExperts];
+  __shared__ int chosen[kMoeMaxTopK];
   __shared__ float dots[kRouteWarps];
   __shared__ unsigned tops[kRouteWarps];
   allow_dependent_launch();
-  const int t = blockIdx.x / kRouteBlocks, part = blockIdx.x % kRouteBlocks;
+  // the first block has to be there before the others write to it: they arrive here and wait
+  // just before they do
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int t = blockIdx.x / blocks, part = blockIdx.x % blocks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = blockIdx.x * kRouteThreads + threadIdx.x; i < n_clear; i += gridDim.x * kRouteThreads) clear[i] = 0;
   const char* xr = static_cast<const char*>(x) + row_offset(t, D, kXBf16);
-  float* mine = logits_all + static_cast<size_t>(t) * E;
   // `share` warps (a power of two) to an expert, experts part, part + 8, ... of the token
-  const int experts = max(1, (E - part + kRouteBlocks - 1) / kRouteBlocks);  // one that is not there at least
+  const int experts = max(1, (E - part + blocks - 1) / blocks);  // one that is not there at least
   int share = 1;
   while (2 * share * experts <= kRouteWarps) share *= 2;
-  float m = 0.0f;
-  bool bad = false;
+  unsigned m = 0u;  // bits of the largest |x|; those of a NaN are larger still
+  bool met = false;
   for (int i0 = 0; i0 < experts; i0 += kRouteWarps / share) {
-    const int want = part + kRouteBlocks * (i0 + warp / share), e = min(want, E - 1);
+    const int want = part + blocks * (i0 + warp / share), e = min(want, E - 1);
     const char* rr = static_cast<const char*>(router) + row_offset(e, D, kRBf16);
     float s = 0.0f;
-    constexpr int kBatch = 4;  // vectors in flight per lane
+    constexpr int kBatch = kXBf16 && kRBf16 ? 8 : 4;  // vectors in flight per lane
     for (int c0 = (warp % share) * 32 + lane; c0 < D / 8; c0 += kBatch * 32 * share) {
-      float a[kBatch][8], b[kBatch][8];
+      Raw8<kXBf16> a[kBatch];
+      Raw8<kRBf16> b[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const int c = min(c0 + 32 * share * u, D / 8 - 1);
-        load8<kXBf16>(xr, c, a[u]);
-        load8<kRBf16>(rr, c, b[u]);
+        a[u] = load_raw8<kXBf16, true>(xr, c);  // kept in this order: all before the first use
+        b[u] = load_raw8<kRBf16, true>(rr, c);
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
+        float x8[8], r8[8];
+        unpack8<kXBf16>(a[u], x8);
+        unpack8<kRBf16>(b[u], r8);
         const bool in = c0 + 32 * share * u < D / 8;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          s = fmaf(a[u][j], in ? b[u][j] : 0.0f, s);
-          bad |= !(fabsf(a[u][j]) <= kFloatMax);
-          m = fmaxf(m, fabsf(a[u][j]));
+          s = fmaf(x8[j], in ? r8[j] : 0.0f, s);
+          m = max(m, __float_as_uint(x8[j]) & 0x7fffffffu);
         }
       }
     }
@@ -145,15 +141,18 @@ moe_route_kernel(const void* __restrict__ x, const void* __restrict__ router, in
       s = 0.0f;
       for (int j = 0; j < share; ++j) s += dots[warp / share * share + j];
     }
-    if (lane == 0 && warp % share == 0 && want < E) __stcg(mine + e, s);
+    if (!met) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    met = true;
+    if (lane == 0 && warp % share == 0 && want < E) st_cluster_f32(smem_u32(logits + want), 0, s);
   }
-  if (bad) record_status(kStatusNonfinite);
-  const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-  if (lane == 0) tops[warp] = top;
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (lane == 0) tops[warp] = m;
   __syncthreads();
-  m = __uint_as_float(__reduce_max_sync(0xffffffffu, tops[lane % kRouteWarps]));
-  const float f = m > 0.0f ? __fdiv_rn(127.0f, m) : 0.0f;
-  for (int c = part * kRouteThreads + threadIdx.x; c < D / 8; c += kRouteBlocks * kRouteThreads) {
+  const float a = __uint_as_float(__reduce_max_sync(0xffffffffu, tops[lane % kRouteWarps]));
+  const bool fine = a <= kFloatMax;
+  if (!fine && threadIdx.x == 0) record_status(kStatusNonfinite);
+  const float f = fine && a > 0.0f ? __fdiv_rn(127.0f, a) : 0.0f;
+  for (int c = part * kRouteThreads + threadIdx.x; c < D / 8; c += blocks * kRouteThreads) {
     float v[8];
     load8<kXBf16>(xr, c, v);
     uint32_t q[2] = {0u, 0u};
@@ -162,12 +161,10 @@ moe_route_kernel(const void* __restrict__ x, const void* __restrict__ router, in
       q[i >> 2] |= (static_cast<uint32_t>(quant_i8(v[i], f)) & 0xffu) << (8 * (i & 3));
     reinterpret_cast<uint2*>(xq + static_cast<size_t>(t) * D)[c] = make_uint2(q[0], q[1]);
   }
-  cluster_barrier();  // the logits of the other blocks
+  cluster_barrier();  // every block's logits are in the first one's shared memory
   if (part != 0) return;
-  if (threadIdx.x == 0) xscale[t] = m > 0.0f ? __fdiv_rn(m, 127.0f) : 0.0f;
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) logits[e] = __ldcg(mine + e);
-  __syncthreads();
-  if (warp == 0) moe_top_k(logits, E, top_k, renorm, ids + t * top_k, weights + t * top_k);
+  if (threadIdx.x == 0) xscale[t] = fine ? __fdiv_rn(a, 127.0f) : 0.0f;
+  moe_top_k<kRouteThreads>(logits, E, top_k, renorm, keys, chosen, ids + t * top_k, weights + t * top_k);
 }
 
 // ------------------------------------------------------------------------------- experts

@@ -25,11 +25,14 @@ template <bool kBf16>
 struct Raw8 {
   uint4 v[kBf16 ? 1 : 2];
 };
-template <bool kBf16>
+template <bool kBf16, bool kStream = false>
 __device__ __forceinline__ Raw8<kBf16> load_raw8(const void* row, int c) {
   Raw8<kBf16> r;
 #pragma unroll
-  for (int i = 0; i < (kBf16 ? 1 : 2); ++i) r.v[i] = reinterpret_cast<const uint4*>(row)[(kBf16 ? 1 : 2) * c + i];
+  for (int i = 0; i < (kBf16 ? 1 : 2); ++i) {
+    const uint4* p = reinterpret_cast<const uint4*>(row) + (kBf16 ? 1 : 2) * c + i;
+    r.v[i] = kStream ? ld_stream_v4(p) : *p;
+  }
   return r;
 }
 template <bool kBf16>
