@@ -28,7 +28,8 @@ EXPORTS = (
     "bitlinear_quantize_acts_absmax", "bitlinear_rescale", "bitlinear_chain_workspace_size",
     "bitlinear_chain_forward", "bitlinear_base3_row_bytes", "bitlinear_pack_base3",
     "bitlinear_forward_base3", "bitlinear_pack_transpose", "bitlinear_backward_workspace_size",
-    "bitlinear_backward", "bitlinear_backward_quantized", "bitlinear_forward_quantized",
+    "bitlinear_backward", "bitlinear_backward_quantized_workspace_size", "bitlinear_backward_quantized",
+    "bitlinear_forward_quantized",
     "bitlinear_rmsnorm_quantize", "bitlinear_rmsnorm_backward_workspace_size",
     "bitlinear_rmsnorm_backward", "bitlinear_moe_workspace_size", "bitlinear_moe_forward",
     "bitlinear_forward", "bitlinear_forward_noalloc", "bitlinear_contract_i32",
@@ -103,6 +104,8 @@ def load_library() -> ctypes.CDLL:
     lib.bitlinear_backward_workspace_size.restype = sz
     lib.bitlinear_backward.argtypes = [p, i, p, p, p, p, p, i, i, i, p, sz, p]
     lib.bitlinear_backward.restype = i
+    lib.bitlinear_backward_quantized_workspace_size.argtypes = [i, i, i]
+    lib.bitlinear_backward_quantized_workspace_size.restype = sz
     lib.bitlinear_backward_quantized.argtypes = [p, p, p, p, p, p, p, i, i, i, p, sz, p]
     lib.bitlinear_backward_quantized.restype = i
     lib.bitlinear_forward_quantized.argtypes = [p, p, p, p, p, i, i, i, i, p, sz, p]
@@ -439,9 +442,11 @@ def backward(x: torch.Tensor, grad_y: torch.Tensor, packedT: torch.Tensor, gamma
 
 def backward_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
     """A caller-owned device workspace for backward and backward_quantized."""
-    n = int(load_library().bitlinear_backward_workspace_size(M, N, K))
+    lib = load_library()
+    n = max(int(lib.bitlinear_backward_workspace_size(M, N, K)),
+            int(lib.bitlinear_backward_quantized_workspace_size(M, N, K)))
     if n == 0:
-        raise BitLinearError(2, "bitlinear_backward_workspace_size")
+        raise BitLinearError(2, "bitlinear_backward_quantized_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
@@ -452,7 +457,7 @@ def backward_quantized(xq: torch.Tensor, scale: torch.Tensor, grad_y: torch.Tens
     (M, K), N, at = xq.shape, grad_y.shape[1], _index(xq, "xq")
     gx = scale.new_empty((M, K)) if need_x else None
     gw = scale.new_empty((N, K)) if need_w else None
-    if ws is None and need_w:
+    if ws is None:
         ws = backward_workspace(M, N, K, xq.device)
     _run((_lib or load_library()).bitlinear_backward_quantized, "bitlinear_backward_quantized", at, stream,
          _take(xq, "xq", (M, K), torch.int8, at), _take(scale, "scale", (M,), torch.float32, at),
@@ -460,7 +465,7 @@ def backward_quantized(xq: torch.Tensor, scale: torch.Tensor, grad_y: torch.Tens
          _take(packedT, "packedT", (K, N // 4), torch.uint8, at),
          _take(gamma, "gamma", (1,), torch.float32, at),
          gx.data_ptr() if need_x else None, gw.data_ptr() if need_w else None, M, N, K,
-         None if ws is None else _take_ws(ws, at), 0 if ws is None else ws.numel())
+         _take_ws(ws, at), ws.numel())
     return gx, gw
 
 

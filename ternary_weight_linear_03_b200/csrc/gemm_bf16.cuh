@@ -46,6 +46,7 @@ constexpr int BP_BYTES = BN * BKE / 4; // 3 KB packed B tile
 constexpr int TMEM_COLS = 512;         // two accumulators of BN columns (a power of two)
 constexpr int THREADS = 384;
 constexpr int MMA_SENTINEL = 10, UNPACK_SENTINEL = 11;
+constexpr int SPLIT = 16;              // stages whose products one accumulator sums (kSplit)
 
 // D fp32 (bits 4-5 = 1), A and B bf16 (bits 7-9 = 1, 10-12 = 1), both K-major, N >> 3 in
 // bits 17-22, M >> 4 in bits 24-28.
@@ -68,11 +69,12 @@ struct Barriers {
 };
 
 // B packed: TMA ring of (A, packed B) plus a ring of unpacked B tiles; else (A, B) by TMA.
-template <bool kPacked>
+constexpr int OUT_STRIDE = 20;          // floats of a row in an epilogue warp's 32 x 16 tile (kSplit)
+template <bool kPacked, bool kSplit = false>
 __host__ __device__ constexpr int smem_bytes() {
   return 1024 + STAGES * A_BYTES +
          (kPacked ? USTAGES * BT_BYTES + STAGES * BP_BYTES : STAGES * BT_BYTES) +
-         static_cast<int>(sizeof(Barriers));
+         (kSplit ? 8 * 32 * OUT_STRIDE * 4 : 0) + static_cast<int>(sizeof(Barriers));
 }
 }  // namespace bf
 
@@ -106,7 +108,12 @@ __device__ __forceinline__ uint32_t trit_pair_bf16(uint32_t t) {
 // tensor maps zero-fill past the end). kPacked: B comes as 2-bit trits [C][J/4] (the
 // library's packed format, rows c) and is unpacked to bf16 here. alpha: device float or
 // null (1). out fp32 [R][C] row-major.
-template <bool kPacked>
+// kSplit (B bf16): the tensor core truncates where it adds to an accumulator, so the error
+// of a long sum grows with its length and not with the root of it. Every SPLIT stages (1024
+// elements) go to a fresh accumulator, and the epilogue, on eight warps with 96 columns each,
+// adds those in registers (4096 tokens: error against 64 bits 4.3e-6 -> 1.1e-6, for the
+// same time). C % 4 == 0.
+template <bool kPacked, bool kSplit = false>
 __global__ void __launch_bounds__(bf::THREADS, 1) gemm_bf16_kernel(
     const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
     const float* __restrict__ alpha_ptr, float* __restrict__ out, int R, int C, int J,
@@ -118,7 +125,9 @@ __global__ void __launch_bounds__(bf::THREADS, 1) gemm_bf16_kernel(
   unsigned char* sA = smem;
   unsigned char* sB = sA + STAGES * A_BYTES;                 // bf16 B tiles (TMA or unpacked)
   unsigned char* sBp = sB + (kPacked ? USTAGES : STAGES) * BT_BYTES;  // packed B (kPacked)
-  Barriers* bar = reinterpret_cast<Barriers*>(sBp + (kPacked ? STAGES * BP_BYTES : 0));
+  float* sOut = reinterpret_cast<float*>(sBp + (kPacked ? STAGES * BP_BYTES : 0));  // kSplit
+  Barriers* bar = reinterpret_cast<Barriers*>(reinterpret_cast<unsigned char*>(sOut) +
+                                              (kSplit ? 8 * 32 * OUT_STRIDE * 4 : 0));
   volatile int* abort_flag = &bar->abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -126,6 +135,8 @@ __global__ void __launch_bounds__(bf::THREADS, 1) gemm_bf16_kernel(
   const int c_tiles = (C + BN - 1) / BN;
   const int num_tiles = r_tiles * c_tiles;
   const int KB = (J + BKE - 1) / BKE;
+  static_assert(!(kPacked && kSplit), "the unpack warps are the split's epilogue warps");
+  const int PER = kSplit ? SPLIT : KB;  // stages of an accumulator
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -138,7 +149,7 @@ __global__ void __launch_bounds__(bf::THREADS, 1) gemm_bf16_kernel(
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bar->tmem_full[b], 1);
-      mbar_init(&bar->tmem_empty[b], 4);
+      mbar_init(&bar->tmem_empty[b], kSplit ? 8 : 4);
     }
     mbar_init(&bar->drain, 1);
     bar->abort = 0;
@@ -193,32 +204,35 @@ __global__ void __launch_bounds__(bf::THREADS, 1) gemm_bf16_kernel(
     uint32_t aph = 0;
     bool ok = true, issued_any = false;
     for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
-      bool got = true;
-      if (lane == 0) got = tc_wait(&bar->tmem_empty[ab], aph ^ 1u, limit_ns, abort_flag);
-      got = __shfl_sync(0xffffffffu, got, 0);
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(ab * BN);
-      for (int kb = 0; kb < KB; ++kb) {
-        // the sentinel has seen the stage land (and its B unpacked); a failed accumulator
-        // wait leaves at the first handoff
-        if (bf_mma_bar_or(!got)) { ok = false; break; }
+      for (int kb0 = 0; kb0 < KB && ok; kb0 += PER) {
+        bool got = true;
+        if (lane == 0) got = tc_wait(&bar->tmem_empty[ab], aph ^ 1u, limit_ns, abort_flag);
+        got = __shfl_sync(0xffffffffu, got, 0);
         tc_fence_after();
-        const uint64_t a_desc = a_desc0 + static_cast<uint64_t>(s * (A_BYTES >> 4));
-        const uint64_t b_desc =
-            b_desc0 + static_cast<uint64_t>((kPacked ? u : s) * (BT_BYTES >> 4));
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(ab * BN);
+        for (int kb = kb0; kb < min(KB, kb0 + PER); ++kb) {
+          // the sentinel has seen the stage land (and its B unpacked); a failed accumulator
+          // wait leaves at the first handoff
+          if (bf_mma_bar_or(!got)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t a_desc = a_desc0 + static_cast<uint64_t>(s * (A_BYTES >> 4));
+          const uint64_t b_desc =
+              b_desc0 + static_cast<uint64_t>((kPacked ? u : s) * (BT_BYTES >> 4));
 #pragma unroll
-        for (int kk = 0; kk < BKE / MMA_K; ++kk)  // 32 bytes of bf16 per MMA
-          mma_bf16_elect(d_tmem, a_desc + static_cast<uint64_t>(kk * 2),
-                         b_desc + static_cast<uint64_t>(kk * 2), IDESC, (kb | kk) != 0 ? 1u : 0u);
-        issued_any = true;
-        mma_commit_elect(&bar->empty_tma[s]);
-        if (kPacked) mma_commit_elect(&bar->empty_unp[u]);
-        if (++s == STAGES) s = 0;
-        if (kPacked && ++u == USTAGES) u = 0;
+          for (int kk = 0; kk < BKE / MMA_K; ++kk)  // 32 bytes of bf16 per MMA
+            mma_bf16_elect(d_tmem, a_desc + static_cast<uint64_t>(kk * 2),
+                           b_desc + static_cast<uint64_t>(kk * 2), IDESC,
+                           (kb != kb0 || kk != 0) ? 1u : 0u);
+          issued_any = true;
+          mma_commit_elect(&bar->empty_tma[s]);
+          if (kPacked) mma_commit_elect(&bar->empty_unp[u]);
+          if (++s == STAGES) s = 0;
+          if (kPacked && ++u == USTAGES) u = 0;
+        }
+        if (!ok) break;
+        mma_commit_elect(&bar->tmem_full[ab]);
+        if (++ab == 2) { ab = 0; aph ^= 1u; }
       }
-      if (!ok) break;
-      mma_commit_elect(&bar->tmem_full[ab]);
-      if (++ab == 2) { ab = 0; aph ^= 1u; }
     }
     if (!ok && issued_any) {
       mma_commit_elect(&bar->drain);
@@ -261,7 +275,66 @@ __global__ void __launch_bounds__(bf::THREADS, 1) gemm_bf16_kernel(
         }
       }
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (kSplit && warp >= 2 && warp < 10) {
+    // ------------------------------------------------------------------ epilogue (kSplit)
+    // a warp reads the TMEM lanes of its quarter (warp % 4); warps 4..7 the first 96 columns
+    const int quarter = warp & 3, col0 = (warp >= 4 && warp < 8) ? 0 : BN / 2;
+    const float alpha = (alpha_ptr != nullptr) ? *alpha_ptr : 1.0f;
+    int ab = 0;
+    uint32_t aph = 0;
+    bool got = true;
+    for (int tile = blockIdx.x; tile < num_tiles && got; tile += gridDim.x) {
+      float sum[BN / 2];
+#pragma unroll
+      for (int j = 0; j < BN / 2; ++j) sum[j] = 0.0f;
+      for (int kb0 = 0; kb0 < KB && got; kb0 += PER) {
+        got = tc_wait(&bar->tmem_full[ab], aph, limit_ns, abort_flag);
+        got = __all_sync(0xffffffffu, got);
+        if (!got) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                               static_cast<uint32_t>(ab * BN + col0);
+#pragma unroll
+        for (int cb = 0; cb < BN / 64; ++cb) {
+          uint32_t v[32];
+          tmem_ld_x32(taddr + cb * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            sum[cb * 32 + j] = __fadd_rn(sum[cb * 32 + j], __uint_as_float(v[j]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->tmem_empty[ab]);
+        if (++ab == 2) { ab = 0; aph ^= 1u; }
+      }
+      if (!got) break;
+      // Through shared memory, 16 columns at a time, so that a row leaves as 64 bytes: a lane
+      // writing its own row sends 16 bytes to each of 32 lines (130 x 3200 x 8640 grad_w,
+      // 1125 tiles of 3 stages: 58 -> 41 us).
+      const int r0 = (tile % r_tiles) * BM + quarter * 32;
+      const int c0 = (tile / r_tiles) * BN + col0;
+      float* stage = sOut + (warp - 2) * 32 * OUT_STRIDE;
+#pragma unroll
+      for (int cb = 0; cb < BN / 2; cb += 16) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          *reinterpret_cast<float4*>(stage + lane * OUT_STRIDE + j) =
+              make_float4(__fmul_rn(sum[cb + j], alpha), __fmul_rn(sum[cb + j + 1], alpha),
+                          __fmul_rn(sum[cb + j + 2], alpha), __fmul_rn(sum[cb + j + 3], alpha));
+        __syncwarp();
+        const int c = c0 + cb + 4 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          const int row = i + (lane >> 2);
+          const float4 v = *reinterpret_cast<const float4*>(stage + row * OUT_STRIDE + 4 * (lane & 3));
+          if (r0 + row < R && c < C)  // C % 4 == 0: four columns are all in or all out
+            *reinterpret_cast<float4*>(out + static_cast<long long>(r0 + row) * C + c) = v;
+        }
+      }
+    }
+  } else if (!kSplit && warp >= 4 && warp < 8) {
     // ------------------------------------------------------------------ epilogue
     const int quarter = warp - 4;
     const int row = quarter * 32 + lane;
@@ -423,6 +496,23 @@ __global__ void __launch_bounds__(256) transpose_bf16_kernel(
       }
     }
     __syncthreads();
+  }
+}
+
+// 2-bit weights -> bf16 codes, `words` words of 16 trits each.
+__global__ void __launch_bounds__(256) unpack_bf16_kernel(const uint32_t* __restrict__ packed,
+                                                          uint4* __restrict__ out, long long words) {
+  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < words;
+       i += static_cast<long long>(gridDim.x) * 256) {
+    const uint32_t word = packed[i];
+    uint32_t o[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {  // trits 2q, 2q + 1: group j = q / 2, bytes 2q % 4 and the next
+      const int m = 2 * q;
+      o[q] = trit_pair_bf16((word >> (2 * (m >> 2) + 8 * (m & 3))) & 0x0303u);
+    }
+    out[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
+    out[2 * i + 1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 

@@ -31,10 +31,12 @@ def test_argument_checks():
     def back(q=FAKE, s=FAKE, gy=FAKE, p=FAKE, g=FAKE, gx=FAKE, gw=FAKE, M=4, N=128, K=64, ws=FAKE, n=1 << 30):
         return lib.bitlinear_backward_quantized(q, s, gy, p, g, gx, gw, M, N, K, ws, n, None)
 
-    for bad in (dict(gy=None), dict(gx=None, gw=None), dict(p=None), dict(g=None), dict(q=None), dict(s=None),
-                dict(ws=None)):
+    for bad in (dict(gy=None), dict(gx=None, gw=None), dict(p=None), dict(g=None), dict(q=None), dict(s=None)):
         assert back(**bad) == 1, bad
-    assert back(N=100) == 2 and back(M=0) == 2 and back(gx=FAKE + 4) == 3 and back(n=16) == 7
+    assert back(N=100) == 2 and back(M=0) == 2 and back(gx=FAKE + 4) == 3
+    need = lib.bitlinear_backward_quantized_workspace_size(4, 128, 64)
+    assert back(n=need - 1) == 7 and back(ws=None) == 7 and back(ws=None, gw=None) == 7
+    assert lib.bitlinear_backward_quantized_workspace_size(4, 100, 64) == 0
 
 
 def _codes(M, K, seed):
@@ -106,7 +108,8 @@ def test_forward_extremes():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,N,K", [(1, 64, 64), (130, 640, 1536), (300, 128, 320)])
+@pytest.mark.parametrize("M,N,K", [(1, 64, 64), (130, 640, 1536), (300, 128, 320), (1025, 128, 192),
+                                   (2600, 192, 64), (33, 2112, 64)])
 def test_backward_matches_oracle(M, N, K):
     q, s = _codes(M, K, M + N + K)
     G = (torch.randn((M, N), generator=syn.gen(M)) * 0.01).bfloat16()
