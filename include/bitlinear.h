@@ -367,8 +367,8 @@ size_t bitlinear_backward_quantized_workspace_size(int M, int N, int K);
 /* bitlinear_backward for a forward that ran on int8 activations (bitlinear_forward_quantized):
  * X~ = bf16(xq * scale) from the codes and scales themselves. Formulas and arguments as there
  * (xq [M][K] and scale [M] are needed for grad_w), with its own workspace, needed for either
- * gradient: the weights are unpacked to bf16 once, and sums of more than 1024 terms are taken in
- * parts of 1024, added in fp32. */
+ * gradient: the weights are unpacked to bf16 once, and sums of more than 512 terms are taken in
+ * parts of 512, added in fp32. */
 bl_status bitlinear_backward_quantized(const int8_t* xq, const float* scale, const void* grad_y,
                                        const uint8_t* packedT, const float* gamma, float* grad_x,
                                        float* grad_w, int M, int N, int K, void* ws,

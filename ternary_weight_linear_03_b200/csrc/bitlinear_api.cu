@@ -1272,7 +1272,7 @@ struct NormArgs {
 
 template <bool kBf16, bool kWBf16, int V>
 bl_status launch_rmsnorm_v(const NormArgs& a, int threads, cudaStream_t s) {
-  return launch_ex(bl::rmsnorm_quant_kernel<kBf16, kWBf16, V>, dim3(a.M), dim3(threads), 0, s, false, a.x, a.r,
+  return launch_ex(bl::rmsnorm_quant_kernel<kBf16, kWBf16, V>, dim3(a.M), dim3(threads), 0, s, true, a.x, a.r,
                    a.w, a.eps, a.K, a.h, a.normed, a.xq, a.scale, a.rstd);
 }
 
@@ -1538,18 +1538,19 @@ bl_status bitlinear_moe_forward(const void* x, int x_dtype, int M, const bl_moe*
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int blocks = 8 * M <= num_sms() ? 8 : 2;  // of a token: one wave of one block per SM
   int* clear = reinterpret_cast<int*>(w.amax);
-  // launched in full order: the kernels of a call before may still use the workspace
   auto route = [&](auto kern) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(M * blocks);
     cfg.blockDim = dim3(bl::kRouteThreads);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = blocks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kern, x, m.router, m.D, m.E, m.top_k, m.renormalize, w.ids, w.weights,
                            w.xq, w.scale, clear, n_clear, blocks) != cudaSuccess)
       return BL_ERR_CUDA;

@@ -46,7 +46,7 @@ constexpr int BP_BYTES = BN * BKE / 4; // 3 KB packed B tile
 constexpr int TMEM_COLS = 512;         // two accumulators of BN columns (a power of two)
 constexpr int THREADS = 384;
 constexpr int MMA_SENTINEL = 10, UNPACK_SENTINEL = 11;
-constexpr int SPLIT = 16;              // stages whose products one accumulator sums (kSplit)
+constexpr int SPLIT = 8;               // stages whose products one accumulator sums (kSplit)
 
 // D fp32 (bits 4-5 = 1), A and B bf16 (bits 7-9 = 1, 10-12 = 1), both K-major, N >> 3 in
 // bits 17-22, M >> 4 in bits 24-28.
@@ -109,7 +109,7 @@ __device__ __forceinline__ uint32_t trit_pair_bf16(uint32_t t) {
 // library's packed format, rows c) and is unpacked to bf16 here. alpha: device float or
 // null (1). out fp32 [R][C] row-major.
 // kSplit (B bf16): the tensor core truncates where it adds to an accumulator, so the error
-// of a long sum grows with its length and not with the root of it. Every SPLIT stages (1024
+// of a long sum grows with its length and not with the root of it. Every SPLIT stages (512
 // elements) go to a fresh accumulator, and the epilogue, on eight warps with 96 columns each,
 // adds those in registers (4096 tokens: error against 64 bits 4.3e-6 -> 1.1e-6, for the
 // same time). C % 4 == 0.

@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kRouteThreads, 1) moe_route_kernel(
   __shared__ int chosen[kMoeMaxTopK];
   __shared__ float dots[kRouteWarps];
   __shared__ unsigned tops[kRouteWarps];
+  grid_dependency_wait();  // the call before may still use the workspace, x may not be there yet
   allow_dependent_launch();
   // the first block has to be there before the others write to it: they arrive here and wait
   // just before they do

@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_quant_kernel(
     void* h, void* normed, int8_t* __restrict__ xq, float* __restrict__ scale,
     float* __restrict__ rstd_out) {
   __shared__ float red_s[32], red_m[32];
+  grid_dependency_wait();
   allow_dependent_launch();  // a kernel that waits for this one may set itself up meanwhile
   const int t = blockIdx.x, T = blockDim.x, nv = K / 8;
   const size_t off = row_offset(t, K, kBf16);
