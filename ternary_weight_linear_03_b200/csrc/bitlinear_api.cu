@@ -1234,7 +1234,7 @@ bl_status launch_few_n(const int8_t* xq, const float* scale, const uint8_t* pack
 bl_status launch_few(const int8_t* xq, const float* scale, const uint8_t* packed,
                      const float* gamma, void* y, int y_dtype, int M, int N, int K,
                      cudaStream_t s) {
-  if (M > 8) return launch_few_n<2, bl::kFour>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
+  if (M > 8) return launch_few_n<2, bl::kTwo>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
   if (M > 4) return launch_few_n<1, bl::kFour>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
   return launch_few_n<1, bl::kPairs>(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
 }
@@ -1588,7 +1588,7 @@ bl_status bitlinear_moe_forward(const void* x, int x_dtype, int M, const bl_moe*
   const double mean = static_cast<double>(M) * m.top_k / m.E;
   st = M <= 4                                          ? launch_moe<1, bl::kPairs>(a, w, s)
        : M <= 8 || mean + 2.0 * std::sqrt(mean) <= 8.0 ? launch_moe<1, bl::kFour>(a, w, s)
-                                                       : launch_moe<2, bl::kFour>(a, w, s);
+                                                       : launch_moe<2, bl::kTwo>(a, w, s);
   if (st != BL_OK) return st;
   const dim3 out((m.D + 255) / 256, M), threads(256);
   return y_dtype == BL_BF16

@@ -39,44 +39,52 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
 //     products of fragment j, plane j is (P_j - P_(j-1)) / 4^j: an even column holds the token's
 //     codes of plane j, the odd one behind it those of plane j + 1, to be subtracted.
 //     3 masks a word (70B up, one token: 15.2 -> 13.8 us with both steps).
-enum PlaneMode : int { kFour = 0, kPairs = 1 };
+//   kTwo, where 16 columns leave no registers for four accumulators: planes 2 and 3 are shifted
+//     onto 0 and 1. 4 masks and a shift a word, but half as much to clear and to add up
+//     (70B down, 16 tokens: 23.7 -> 22.3 us; 64 tokens of 8 wide experts: 137 -> 122 us).
+enum PlaneMode : int { kFour = 0, kPairs = 1, kTwo = 2 };
+__host__ __device__ constexpr int planes(int mode) { return mode == kTwo ? 2 : 4; }
 
 template <int NT, int MODE>
-__device__ __forceinline__ void ternary_step(int (&acc)[4][NT][4], const uint4& wa,
+__device__ __forceinline__ void ternary_step(int (&acc)[planes(MODE)][NT][4], const uint4& wa,
                                              const uint4& wb, const uint4 (&q)[NT][4]) {
 #pragma unroll
   for (int i = 0; i < 4; i += 2)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t m = MODE == kPairs ? (j == 3 ? 0xffffffffu : ((4u << (2 * j)) - 1u) * 0x01010101u)
+                         : MODE == kTwo ? 0x03030303u << (2 * (j & 1))
                                         : 0x03030303u << (2 * j);
-      const uint32_t a0 = word_of(wa, i) & m, a1 = word_of(wb, i) & m;
-      const uint32_t a2 = word_of(wa, i + 1) & m, a3 = word_of(wb, i + 1) & m;
+      const int sh = (MODE == kTwo && j > 1) ? 4 : 0;
+      const uint32_t a0 = (word_of(wa, i) >> sh) & m, a1 = (word_of(wb, i) >> sh) & m;
+      const uint32_t a2 = (word_of(wa, i + 1) >> sh) & m, a3 = (word_of(wb, i + 1) >> sh) & m;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        mma_u8s8(acc[j][n], a0, a1, a2, a3, word_of(q[n][i], j), word_of(q[n][i + 1], j));
+        mma_u8s8(acc[MODE == kTwo ? j & 1 : j][n], a0, a1, a2, a3, word_of(q[n][i], j), word_of(q[n][i + 1], j));
     }
 }
 // The exact sum: of column e & 1, or (kPairs) of the token of both columns (e even).
 template <int NT, int MODE>
-__device__ __forceinline__ int ternary_sum(const int (&acc)[4][NT][4], int n, int e) {
+__device__ __forceinline__ int ternary_sum(const int (&acc)[planes(MODE)][NT][4], int n, int e) {
   if constexpr (MODE == kPairs)
     return acc[0][n][e] + ((acc[1][n][e] - acc[0][n][e + 1]) >> 2) +
            ((acc[2][n][e] - acc[1][n][e + 1]) >> 4) + ((acc[3][n][e] - acc[2][n][e + 1]) >> 6);
+  else if constexpr (MODE == kTwo)
+    return acc[0][n][e] + (acc[1][n][e] >> 2);
   else
     return acc[0][n][e] + (acc[1][n][e] >> 2) + (acc[2][n][e] >> 4) + (acc[3][n][e] >> 6);
 }
 // Clears the sums, minus[n] (the negative sum of codes) for the columns that u = c + 1 wants
 // it taken off: in kPairs the even ones.
 template <int NT, int MODE>
-__device__ __forceinline__ void ternary_clear(int (&acc)[4][NT][4], const int (&minus)[NT][2]) {
+__device__ __forceinline__ void ternary_clear(int (&acc)[planes(MODE)][NT][4], const int (&minus)[NT][2]) {
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       acc[0][n][e] = minus[n][e & 1];
 #pragma unroll
-      for (int j = 1; j < 4; ++j) acc[j][n][e] = 0;
+      for (int j = 1; j < planes(MODE); ++j) acc[j][n][e] = 0;
     }
 }
 // minus[] from each lane's sum of the codes it loaded for token n (of column 8 n + g, or
@@ -98,7 +106,7 @@ __device__ __forceinline__ int dot_ones(const uint4& v, int sum) {
 // Adds a tile's sums of this warp to those of its block, to[row of the tile][column], for the
 // columns below `valid`.
 template <int NT, int MODE>
-__device__ __forceinline__ void ternary_add(const int (&acc)[4][NT][4], int* to, int valid) {
+__device__ __forceinline__ void ternary_add(const int (&acc)[planes(MODE)][NT][4], int* to, int valid) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -251,7 +259,7 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 2) few_tokens_kernel(
   for (int i0 = 0; i0 < count; i0 += kFewRound) {
     const int i1 = min(count, i0 + kFewRound);
     for (int i = i0; i < i1; ++i) {
-      int acc[4][NT][4];
+      int acc[planes(MODE)][NT][4];
       ternary_clear<NT, MODE>(acc, minus);
       cp_async_wait<kAhead - 1>();
 #pragma unroll

@@ -333,7 +333,10 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_expert_kernel(const MoeArg
   start(fr);
   MoeRun run = fr;
   const uint32_t ring = smem_u32(ring_all) + warp * kMoeRingBytes + lane * 16;
-  auto fetch = [&](uint32_t slot) {
+  const ptrdiff_t other = kDown ? 0 : p.up - p.gate;  // from a tile of gate to that of up
+  const uint8_t* f_ptr = nullptr;  // this lane's row of the tile to fetch (of gate or down)
+  int f_chunk = 0;
+  auto seek = [&]() {
     while (open(fr) && f_tile >= fr.tiles) {  // runs with fewer tiles than warps
       f_tile = wr;
       if (++f_turn >= p.passes) {
@@ -341,24 +344,30 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_expert_kernel(const MoeArg
         next(fr);
       }
     }
-    if (open(fr)) {
-      const uint8_t* w = kDown ? p.down : f_mat ? p.up : p.gate;
-      const int c = 4 * S * (f_turn * p.wk + wk) + t4;
-      const uint8_t* a = w + groups.expert[fr.a] * matrix + ((fr.tile + f_tile) * 16 + g) * pitch;
+    f_ptr = nullptr;
+    if (!open(fr)) return;
+    f_chunk = 4 * S * (f_turn * p.wk + wk) + t4;
+    f_ptr = (kDown ? p.down : p.gate) + groups.expert[fr.a] * matrix + ((fr.tile + f_tile) * 16 + g) * pitch;
+  };
+  auto fetch = [&](uint32_t slot) {
+    if (f_ptr) {
+      const uint8_t* a = f_mat ? f_ptr + other : f_ptr;
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        const int at = 16 * min(c + 4 * s, chunks - 1);
+        const int at = 16 * min(f_chunk + 4 * s, chunks - 1);
         cp_async16(slot + s * 1024, a + at);
         cp_async16(slot + s * 1024 + 512, a + 8 * pitch + at);
       }
       if (++f_mat == kMats) {
         f_mat = 0;
         f_tile += WR;
+        if (f_tile < fr.tiles) f_ptr += 16 * WR * pitch; else seek();
       }
     }
     cp_async_commit();
   };
-#pragma unroll
+  seek();
+#pragma unroll 1
   for (int i = 0; i < kAhead; ++i) fetch(ring + i * S * 1024);
   if (kDown) grid_dependency_wait();
   // ---- the runs
@@ -408,7 +417,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_expert_kernel(const MoeArg
       for (int i = wr; i < run.tiles; i += WR)
 #pragma unroll 1
         for (int m = 0; m < kMats; ++m) {
-          int acc[4][NT][4];
+          int acc[planes(MODE)][NT][4];
           ternary_clear<NT, MODE>(acc, minus);
           cp_async_wait<kAhead - 1>();
 #pragma unroll

@@ -172,6 +172,30 @@ def test_nonfinite_rows_are_reported_and_the_others_stay():
 
 
 @pytest.mark.gpu
+def test_experts_beyond_4_gb():
+    """Expert 299's matrices begin past 2^32 bytes of each stack (16.8 MB an expert); all others are
+    zero. The same tokens through a layer of that expert alone give the same bits."""
+    E, D, F = 300, 16384, 4096
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def stack(N, K):
+        t = torch.full((E, N, K // 4), 0x55, dtype=torch.uint8, device="cuda")  # every trit 0
+        u = torch.randint(0, 3, (4, N, K // 4), generator=g, device="cuda", dtype=torch.uint8)
+        t[E - 1] = u[0] | u[1] << 2 | u[2] << 4 | u[3] << 6
+        return t, torch.full((E,), 0.02, device="cuda")
+
+    gate, up, down = stack(F, D), stack(F, D), stack(D, F)
+    router = torch.zeros((E, D), device="cuda")
+    router[E - 1, 0] = 1.0
+    x = torch.randn((3, D), generator=g, device="cuda").bfloat16()
+    x[:, 0] = 2.0
+    layer = bl.MoeLayer(router, *gate, *up, *down, top_k=1)
+    only = bl.MoeLayer(router[-1:].contiguous(), *[t[-1:].clone() for p in (gate, up, down) for t in p], top_k=1)
+    y = bl.moe_forward(x, layer)
+    assert torch.equal(y, bl.moe_forward(x, only)) and (y != 0).any() and bl.get_device_status() == 0
+
+
+@pytest.mark.gpu
 def test_same_bits_in_any_batch_and_again():
     """A token's output does not depend on the tokens beside it, nor on what the workspace held."""
     layer = _layer(8, 512, 704, seed=4, top_k=3)

@@ -146,6 +146,21 @@ def test_norm_edge_rows():
 
 
 @pytest.mark.gpu
+def test_norm_writes_its_own_rows_only():
+    """Outputs that are the first rows of larger buffers: what lies behind stays."""
+    M, K = 5, 1536
+    x, r, w = _rows(M, K, BF16, 11, True)
+    bufs = [torch.full((M + 1, K), 3, dtype=t, device="cuda") for t in (torch.int8, BF16, BF16)]
+    vecs = [torch.full((M + 4,), 3.0, device="cuda") for _ in range(2)]
+    bl.rmsnorm_quantize(x.cuda(), w.cuda(), r.cuda(), xq=bufs[0][:M], h=bufs[1][:M], normed=bufs[2][:M],
+                        scale=vecs[0][:M], rstd=vecs[1][:M])
+    for t in bufs:
+        assert (t[M] == 3).all() and not (t[:M] == 3).all()
+    for t in vecs:
+        assert (t[M:] == 3).all() and not (t[:M] == 3).any()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), 3e38])
 def test_norm_reports_nonfinite_rows(bad):
     x = torch.ones((3, 128))
