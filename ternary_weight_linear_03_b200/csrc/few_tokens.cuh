@@ -5,7 +5,7 @@
 // The order of k inside a product is free as long as both operands use the same one, so the
 // fragments are taken as the packed format has them: lane (g, t) = (lane / 4, lane % 4) loads
 // 16 bytes (64 trits) of rows g and g + 8; plane j of each 4-byte word is one register of the
-// weight fragment (a shift and a mask), and the 4 codes that belong to it, 4 consecutive
+// weight fragment (one mask), and the 4 codes that belong to it, 4 consecutive
 // bytes of token g, one register of the token fragment. Four lanes cover 256 trits.
 #pragma once
 
@@ -38,7 +38,7 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
 //     0 .. j, w & (4^(j+1) - 1), so the last is the word itself and needs no mask. With P_j the
 //     products of fragment j, plane j is (P_j - P_(j-1)) / 4^j: an even column holds the token's
 //     codes of plane j, the odd one behind it those of plane j + 1, to be subtracted.
-//     3 masks a word (70B up, one token: 15.2 -> 13.8 us with both steps).
+//     3 masks a word (70B up, one token, from shifted planes: 15.2 -> 13.2 us).
 //   kTwo, where 16 columns leave no registers for four accumulators: planes 2 and 3 are shifted
 //     onto 0 and 1. 4 masks and a shift a word, but half as much to clear and to add up
 //     (70B down, 16 tokens: 23.7 -> 22.3 us; 64 tokens of 8 wide experts: 137 -> 122 us).
@@ -176,17 +176,22 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int t) {
   exchange(v[2], v[3], t & 1, 1);
 }
 
-// y[t,n] = fl(float(sum_k c q) fl(scale_t gamma)) for M <= 8 NT tokens (4 in
-// kPairs). Bound by the packed weights' bytes. K is split over all warps of a cluster of blocks, few_steps steps of 256 to one,
-// so that a warp can keep its part of every token in registers for the whole kernel: the
-// codes are read once per cluster, not once per block (they are the same lines for
-// everybody, and L2 hands out one line at a time), and the loop has no shared-memory reads.
-// Each warp then streams its columns of the cluster's row tiles through a ring of its own in
-// shared memory (a lane reads back what it copied itself, so nobody else is waited for), and
-// adds a tile's integer sums to the block's (exact in any order): no warp waits for another
-// before the join. The ring holds what the memory delivers while the codes arrive. The stream has no bounds to check: rows past N and
-// chunks past K read the last ones, and meet outputs that are not written and codes that
-// are zero.
+// y[t,n] = fl(float(sum_k c q) fl(scale_t gamma)) for M <= 8 NT tokens (4 in kPairs).
+// Bound by the packed weights' bytes up to 8 tokens (70B up, 28672 x 8192: 13.2 us at one token,
+// 14.8 at eight; 4.4 TB/s with launch and prologue, the loop itself runs at the memory's pace),
+// by the matrix instructions' share beyond (20.3 us at sixteen; 70B down 22.3 us).
+// K is split over all warps of a cluster of blocks, few_steps steps of 256 to one, so that a
+// warp can keep its part of every token in registers for the whole kernel: the codes are
+// read once per cluster, not once per block (every block asks for the same lines, and with all
+// of them staged in every block's shared memory 8 tokens of 8192 x 8192 took 15.5 us instead of
+// 7.0), and the loop has no shared-memory reads of codes. Each warp then streams its columns of
+// the cluster's row tiles through a ring of its own in shared memory (a lane reads back what it
+// copied itself, so nobody else is waited for), and adds a tile's integer sums to the block's
+// (exact in any order): no warp waits for another before the join. The ring holds what the
+// memory delivers while the codes arrive. The stream has no bounds to check: rows past N and
+// chunks past K read the last ones, and meet outputs that are not written and codes that are
+// zero. Nothing is read ahead of the wait for the kernel before, which may be the one that wrote
+// the weights (reading them ahead would save 1.3 us).
 template <int NT, int MODE, bool kOBf16>
 __global__ void __launch_bounds__(32 * kFewMaxWarps, 2) few_tokens_kernel(
     const int8_t* __restrict__ xq, const float* __restrict__ scale, const uint8_t* __restrict__ packed,

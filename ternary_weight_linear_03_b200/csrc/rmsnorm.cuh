@@ -8,7 +8,8 @@
 // rstd is one positive factor per row, so it cancels out of the codes: max |n| = rstd a and
 // n / max |n| = p / a. Both row statistics (the sum of squares and a) are therefore taken in
 // the same pass over the registers that hold the row, and one block barrier joins them; x
-// and r are read once, h and the codes written once.
+// and r are read once, h and the codes written once (4096 x 8192 bf16 with a residual: 40.8 us,
+// 5.8 TB/s of the 6.5 that a copy reaches; one row: 3.1 us, launch included).
 #pragma once
 
 #include "act_quant.cuh"
@@ -97,7 +98,7 @@ __device__ __forceinline__ void store8(void* row, int c, const float (&v)[8]) {
 
 // quant_i8 of four values for an r that is finite and 127 / a rounded, |v| <= a: then |v r| is
 // 127 at most after rounding, and adding 1.5 * 2^23 leaves the rounded code in the low byte.
-// Half of quant_i8's instructions, none of them a conversion (4096 x 8192: 42.9 -> 40.6 us).
+// Half of quant_i8's instructions, none of them a conversion (4096 x 8192: 43.0 -> 40.8 us).
 __device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d, float r) {
   const float k = 12582912.0f;
   const uint32_t ta = __float_as_uint(__fadd_rn(__fmul_rn(a, r), k));
