@@ -94,8 +94,8 @@ typedef struct {
 } bl_moe;
 
 /* Device bytes of workspace that bitlinear_quantize_weights (for N x K) and
- * bitlinear_forward / bitlinear_contract_i32 (for M x N x K) need; the largest of the
- * three. Pure host function. Returns 0 for shapes the library rejects. */
+ * bitlinear_forward / bitlinear_contract_i32 / bitlinear_forward_quantized (for M x N x K)
+ * need; the largest of the four. Pure host function. Returns 0 for shapes the library rejects. */
 size_t bitlinear_workspace_size(int M, int N, int K);
 
 /* Absmean ternary weight quantization (LIT-380 bullet 1; Abstract of the searcharxiv.com

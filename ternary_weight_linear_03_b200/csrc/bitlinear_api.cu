@@ -512,6 +512,21 @@ size_t fwd_ws_bytes(int M, int N, int K) {
   return fwd_ws_layout(nullptr, M, K).bytes;
 }
 
+constexpr int kFewMaxM = 16;  // M above this runs the forward's tensor-core kernels
+// Whether a call runs the few-token kernel: a cluster's warps hold every code in registers.
+bool use_few(int M, int K) {
+  return M <= kFewMaxM &&
+         K <= 256 * bl::few_steps(M <= 8 ? 1 : 2) * bl::kFewMaxWarps * bl::kFewMaxCluster;
+}
+
+// Workspace bytes of bitlinear_forward_quantized: none for the few-token kernel; else those of the
+// tensor-core paths, also where bitlinear_forward has its GEMV (few tokens of very wide rows).
+size_t quantized_ws_bytes(int M, int N, int K) {
+  if (use_few(M, K)) return 0;
+  if (M <= kSkinnyMaxM) return skinny_ws_layout(nullptr, M, N, K, skinny_plan(M, N, K)).bytes;
+  return fwd_ws_layout(nullptr, M, K).bytes;
+}
+
 bl_status launch_act_quant(const void* x, int x_dtype, int M, int K, int8_t* xq, float* scale,
                            int* rowsum, cudaStream_t s, uint4* zero = nullptr,
                            long long zero_n16 = 0) {
@@ -663,7 +678,8 @@ extern "C" {
 
 size_t bitlinear_workspace_size(int M, int N, int K) {
   if (!shape_ok(M, N, K)) return 0;
-  const size_t need = std::max(wq_ws_bytes(static_cast<long long>(N) * K), fwd_ws_bytes(M, N, K));
+  const size_t need = std::max({wq_ws_bytes(static_cast<long long>(N) * K), fwd_ws_bytes(M, N, K),
+                                quantized_ws_bytes(M, N, K)});
   return align_up(need, 256);
 }
 
@@ -1159,13 +1175,6 @@ bl_status bitlinear_contract_i32(const int8_t* xq, const uint8_t* packed, int32_
 namespace {
 
 // ------------------------------------------------------------------ layer on int8 codes
-constexpr int kFewMaxM = 16;  // M above this runs the forward's tensor-core kernels
-
-// Whether a call runs the few-token kernel: a cluster's warps hold every code in registers.
-bool use_few(int M, int K) {
-  return M <= kFewMaxM &&
-         K <= 256 * bl::few_steps(M <= 8 ? 1 : 2) * bl::kFewMaxWarps * bl::kFewMaxCluster;
-}
 
 // Clusters of the few-token kernel that the current device holds at once: a second wave would
 // wait for the first.
@@ -1465,7 +1474,7 @@ bl_status bitlinear_forward_quantized(const int8_t* xq, const float* scale, cons
   if (use_few(M, K)) return launch_few(xq, scale, packed, gamma, y, y_dtype, M, N, K, s);
   if (!ws) return BL_ERR_WORKSPACE;
   if (!aligned16(ws)) return BL_ERR_MISALIGNED;
-  if (ws_bytes < fwd_ws_bytes(M, N, K)) return BL_ERR_WORKSPACE;
+  if (ws_bytes < quantized_ws_bytes(M, N, K)) return BL_ERR_WORKSPACE;
   FwdWs w = fwd_ws_layout(ws, M, K);
   uint4* zero = nullptr;
   long long zero_n16 = 0;

@@ -28,6 +28,13 @@ def test_argument_checks():
         assert call(**bad) == 3, bad
     assert call(M=300, ws=None) == 7 and call(M=300, n=16) == 7 and call(M=300, ws=FAKE + 8) == 3
 
+    # rows too wide for the few-token kernel: the workspace covers the tensor-core path's staging
+    # (8 bytes a token beside the split sums) although bitlinear_forward would need none
+    need = lib.bitlinear_workspace_size(2, 1 << 13, 65536 + 64)
+    assert need >= 2 * (65536 + 64) + 2 * 8
+    assert call(M=2, N=1 << 13, K=65536 + 64, ws=None) == 7
+    assert call(M=2, N=1 << 13, K=65536 + 64, n=2 * (65536 + 64)) == 7
+
     def back(q=FAKE, s=FAKE, gy=FAKE, p=FAKE, g=FAKE, gx=FAKE, gw=FAKE, M=4, N=128, K=64, ws=FAKE, n=1 << 30):
         return lib.bitlinear_backward_quantized(q, s, gy, p, g, gx, gw, M, N, K, ws, n, None)
 
@@ -48,7 +55,8 @@ def _codes(M, K, seed):
 
 SHAPES = [(M, N, K) for M in (1, 2, 7, 8, 9, 16, 17, 40) for N, K in ((37, 64), (300, 192), (640, 1536))] + [
     (1, 1, 64), (3, 129, 320), (5, 8640, 3200), (16, 3200, 8640), (12, 1000, 28672), (15, 64, 28672),
-    (257, 200, 448), (4, 70, 65536), (16, 70, 65536)]
+    (257, 200, 448), (4, 70, 65536), (16, 70, 65536),
+    (1, 70, 65600), (2, 300, 98304)]
 
 
 @pytest.mark.gpu
