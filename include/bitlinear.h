@@ -360,8 +360,8 @@ bl_status bitlinear_backward(const void* x, int x_dtype, const void* grad_y,
                              float* grad_w, int M, int N, int K, void* ws, size_t ws_bytes,
                              void* stream);
 
-/* Workspace bytes of bitlinear_backward_quantized (0 for shapes it rejects): the larger of its
- * two gradients' operands in bf16. Pure host function. */
+/* Workspace bytes of bitlinear_backward_quantized (0 for shapes it rejects): both
+ * gradients' operands in bf16. Pure host function. */
 size_t bitlinear_backward_quantized_workspace_size(int M, int N, int K);
 
 /* bitlinear_backward for a forward that ran on int8 activations (bitlinear_forward_quantized):

@@ -876,22 +876,25 @@ BwdWs bwd_ws_layout(void* base, int M, int N, int K) {
   return w;
 }
 
-// Workspace of bitlinear_backward_quantized: [G^T][X~^T] or, used after them, the bf16 codes of
-// the transposed weights [K][N] in the same bytes.
+// Workspace of bitlinear_backward_quantized: [G^T][X~^T][bf16 codes of the transposed weights].
 struct BwdqWs {
-  BwdWs b;
-  __nv_bfloat16* wT;
+  __nv_bfloat16 *gT, *xT, *wT;
+  int Mp;
   size_t bytes;
 };
 BwdqWs bwdq_ws_layout(void* base, int M, int N, int K) {
   BwdqWs w{};
-  w.b.Mp = (M + 7) / 8 * 8;
-  const size_t g = align_up(static_cast<size_t>(N) * w.b.Mp * 2, 256);
-  const size_t x = align_up(static_cast<size_t>(K) * w.b.Mp * 2, 256);
-  w.b.gT = static_cast<__nv_bfloat16*>(base);
-  w.b.xT = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(base) + g);
-  w.wT = static_cast<__nv_bfloat16*>(base);
-  w.bytes = std::max(g + x, align_up(static_cast<size_t>(K) * N * 2, 256));
+  w.Mp = (M + 7) / 8 * 8;
+  char* p = static_cast<char*>(base);
+  auto take = [&p](size_t elements) {
+    char* q = p;
+    p += align_up(elements * 2, 256);
+    return reinterpret_cast<__nv_bfloat16*>(q);
+  };
+  w.gT = take(static_cast<size_t>(N) * w.Mp);
+  w.xT = take(static_cast<size_t>(K) * w.Mp);
+  w.wT = take(static_cast<size_t>(K) * N);
+  w.bytes = static_cast<size_t>(p - static_cast<char*>(base));
   return w;
 }
 
@@ -902,7 +905,6 @@ int grid_for(long long work, int per_block) {
 
 // grad_w = G^T X~ from the int8 codes and scales: both operands transposed into the
 // workspace, then the contraction over the tokens.
-template <bool kSplit>
 bl_status launch_grad_w(const int8_t* xq, const float* scale, const void* grad_y, float* grad_w,
                         int M, int N, int K, const BwdWs& w, cudaStream_t s) {
   const int tiles_g = ((w.Mp + 63) / 64) * (N / 64);
@@ -911,7 +913,7 @@ bl_status launch_grad_w(const int8_t* xq, const float* scale, const void* grad_y
   const int tiles_x = ((w.Mp + 63) / 64) * (K / 64);
   bl::transpose_bf16_kernel<1><<<grid_for(tiles_x, 1), 256, 0, s>>>(xq, scale, w.xT, M, K, w.Mp);
   if (launch_status() != BL_OK) return BL_ERR_CUDA;
-  return launch_gemm_bf16<false, kSplit>(w.gT, w.xT, nullptr, grad_w, N, K, w.Mp, s);
+  return launch_gemm_bf16<false>(w.gT, w.xT, nullptr, grad_w, N, K, w.Mp, s);
 }
 
 }  // namespace
@@ -953,7 +955,7 @@ bl_status bitlinear_backward(const void* x, int x_dtype, const void* grad_y,
     if (ws_bytes < w.bytes) return BL_ERR_WORKSPACE;
     bl_status st = launch_act_quant(x, x_dtype, M, K, w.f.xq, w.f.scale, nullptr, s);
     if (st != BL_OK) return st;
-    st = launch_grad_w<false>(w.f.xq, w.f.scale, grad_y, grad_w, M, N, K, w, s);
+    st = launch_grad_w(w.f.xq, w.f.scale, grad_y, grad_w, M, N, K, w, s);
     if (st != BL_OK) return st;
   }
   if (grad_x) return launch_gemm_bf16<true>(grad_y, packedT, gamma, grad_x, M, K, N, s);
@@ -979,19 +981,22 @@ bl_status bitlinear_backward_quantized(const int8_t* xq, const float* scale, con
   const BwdqWs w = bwdq_ws_layout(ws, M, N, K);
   if (!ws || ws_bytes < w.bytes) return BL_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (grad_w) {
-    const bl_status st = launch_grad_w<true>(xq, scale, grad_y, grad_w, M, N, K, w.b, s);
-    if (st != BL_OK) return st;
-  }
-  if (!grad_x) return BL_OK;
   // The weights as bf16 once, rather than tile by tile inside the contraction, which paces it at
   // any number of tokens (grad_x of 4096 x 4096 x 1536: 105 -> 52 us with the unpacking; both
   // gradients of 64 x 1536 x 1536: 32.7 -> 23.8, of 130 x 3200 x 8640: 80 -> 73.6).
-  const long long words = static_cast<long long>(K) * (N / 16);
-  bl::unpack_bf16_kernel<<<grid_for(words, 256), 256, 0, s>>>(
-      reinterpret_cast<const uint32_t*>(packedT), reinterpret_cast<uint4*>(w.wT), words);
+  const long long rows = (w.Mp + 63) / 64, tiles_g = grad_w ? rows * (N / 64) : 0,
+                  tiles_x = grad_w ? rows * (K / 64) : 0,
+                  words = grad_x ? static_cast<long long>(K) * (N / 16) : 0;
+  bl::grad_operands_kernel<<<grid_for(tiles_g + tiles_x + (words + bl::kUnpackWords - 1) / bl::kUnpackWords, 1),
+                             256, 0, s>>>(grad_y, xq, scale, reinterpret_cast<const uint32_t*>(packedT), w.gT,
+                                          w.xT, reinterpret_cast<uint4*>(w.wT), M, N, K, w.Mp, tiles_g, tiles_x,
+                                          words);
   if (launch_status() != BL_OK) return BL_ERR_CUDA;
-  return launch_gemm_bf16<false, true>(grad_y, w.wT, gamma, grad_x, M, K, N, s);
+  if (grad_w) {
+    const bl_status st = launch_gemm_bf16<false, true>(w.gT, w.xT, nullptr, grad_w, N, K, w.Mp, s);
+    if (st != BL_OK) return st;
+  }
+  return grad_x ? launch_gemm_bf16<false, true>(grad_y, w.wT, gamma, grad_x, M, K, N, s) : BL_OK;
 }
 
 }  // extern "C"
@@ -1373,7 +1378,7 @@ bl_status moe_check(int M, const bl_moe* m) {
   if (m->act != BL_ACT_SILU && m->act != BL_ACT_RELU2) return BL_ERR_INVALID_ARG;
   if (M < 1 || M > bl::kMoeMaxTokens || m->E < 1 || m->E > bl::kMoeMaxExperts || m->top_k < 1 ||
       m->top_k > bl::kMoeMaxTopK || m->top_k > m->E || m->D % 64 != 0 || m->F % 64 != 0 ||
-      m->F < 64 || !shape_ok(M * m->top_k, m->F, m->D) || !shape_ok(M * m->top_k, m->D, m->F))
+      m->F < 64 || m->D > bl::kMoeMaxWidth || m->F > bl::kMoeMaxWidth || !shape_ok(M * m->top_k, m->F, m->D) || !shape_ok(M * m->top_k, m->D, m->F))
     return BL_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(m->router) || !aligned16(m->gate) || !aligned16(m->up) || !aligned16(m->down) ||
       !aligned16(m->gate_gamma) || !aligned16(m->up_gamma) || !aligned16(m->down_gamma))

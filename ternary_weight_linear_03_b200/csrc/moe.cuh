@@ -14,6 +14,7 @@ namespace bl {
 constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxExperts = 512;
 constexpr int kMoeMaxTopK = 16;
+constexpr int kMoeMaxWidth = 16384;  // of x and of an expert
 
 enum MoeAct : int { kActSilu = 0, kActRelu2 = 1 };
 

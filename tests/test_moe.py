@@ -44,7 +44,7 @@ def test_argument_checks():
                 dict(down_gamma=None), dict(router_dtype=2), dict(act=2), dict(act=-1)):
         assert call(**bad) == 1, bad
     for bad in (dict(M=0), dict(M=65), dict(E=0), dict(E=513), dict(top_k=0), dict(top_k=9), dict(D=100),
-                dict(D=0), dict(F=0), dict(F=96), dict(E=64, top_k=17), dict(D=65536, F=65536)):
+                dict(D=0), dict(F=0), dict(F=96), dict(E=64, top_k=17), dict(D=65536, F=65536), dict(D=16448), dict(F=16448)):
         assert call(**bad) == 2, bad
     for bad in (dict(x=FAKE + 8), dict(y=FAKE + 8), dict(ws=FAKE + 8), dict(router=FAKE + 2),
                 dict(gate=FAKE + 4), dict(up=FAKE + 4), dict(down=FAKE + 4), dict(gate_gamma=FAKE + 4),
