@@ -159,25 +159,25 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_quant_kernel(
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         ss = fmaf(p[i], p[i], ss);
-        m = fmaxf(m, fabsf(__fmul_rn(p[i], g[i])));
+        m = max_nan(m, fabsf(__fmul_rn(p[i], g[i])));  // a NaN of the gain is in p alone
       }
     }
   }
   ss = warp_sum(ss);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = T >> 5;
   if (lane == 0) { red_s[warp] = ss; red_m[warp] = m; }
   __syncthreads();
   ss = warp_sum(lane < warps ? red_s[lane] : 0.0f);
   m = lane < warps ? red_m[lane] : 0.0f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float rstd =
       __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(K)), eps)));
   const float f = (m > 0.0f) ? __fdiv_rn(127.0f, m) : 0.0f;
   if (threadIdx.x == 0) {
-    // NaN never wins fmaxf, but reaches the sum of squares
+    // NaN or infinite: x or the residual by either, the gain by m
     if (!(ss <= kFloatMax) || !(m <= kFloatMax)) record_status(kStatusNonfinite);
     scale[t] = (m > 0.0f) ? __fdiv_rn(__fmul_rn(m, rstd), 127.0f) : 0.0f;
     if (rstd_out) rstd_out[t] = rstd;

@@ -232,3 +232,21 @@ def test_backward_matches_differences():
         e[k] = step
         want = (loss(h64, w.double() + e) - loss(h64, w.double() - e)) / (2 * step)
         assert abs(gw[k].item() - want.item()) <= 1e-4 * (1 + abs(want.item()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wtype", [F32, BF16])
+@pytest.mark.parametrize("K", [128, 1536, 28672])
+@pytest.mark.parametrize("bad,under", [(float("nan"), 1.0), (float("nan"), 0.0), (float("inf"), 1.0),
+                                       (float("inf"), 0.0), (-float("inf"), 0.0)])
+def test_norm_reports_nonfinite_gains(bad, under, K, wtype):
+    """A NaN in the gain, or an infinite gain over a zero, makes p NaN and leaves the sum of squares finite."""
+    for dtype in (F32, BF16):
+        x = torch.ones((3, K), dtype=dtype)
+        x[:, K - 3] = under
+        w = torch.ones(K)
+        w[K - 3] = bad
+        bl.rmsnorm_quantize(x.cuda(), w.to(wtype).cuda())
+        assert bl.get_device_status() == 6
+        bl.rmsnorm_quantize(x.cuda(), torch.ones(K, dtype=wtype).cuda())
+        assert bl.get_device_status() == 0
