@@ -6,6 +6,8 @@
 // A pair p = t top_k + s is slot s of token t.
 #pragma once
 
+#include <type_traits>
+
 #include "few_tokens.cuh"
 #include "rmsnorm.cuh"
 
@@ -76,10 +78,12 @@ __device__ __forceinline__ void moe_top_k(const float* logits, int E, int top_k,
 // One cluster of `blocks` blocks (8, or 2 when there are more tokens than eighths of the GPU) per
 // token. Each block takes its share of the experts' logits and of the row's codes, and the
 // first one, to whose shared memory the others send theirs, chooses. Also clears what the next
-// kernels add to. Bound by latency, so all of the router is asked for at once: as many warps
-// share an expert's dot product as there are, with eight vectors of x and of the router in
-// flight per lane (64 experts of 4096, one token: 17 -> 10 thousand cycles with the choice in
-// one pass of ranks).
+// kernels add to. A dot product is the sum of `share` warps' parts, in order, and a part that of
+// 32 lanes' vectors; share follows from E alone, so a token's logits, and with them its experts,
+// have the same bits whatever other tokens there are. Bound by latency, so all of the router is
+// asked for at once: share is what spreads the experts over all warps of 8 blocks, with eight
+// vectors of the router in flight per lane (64 experts of 4096, one token: 17 -> 10 thousand
+// cycles with the choice in one pass of ranks).
 constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
 
@@ -91,65 +95,85 @@ __global__ void __launch_bounds__(kRouteThreads, 1) moe_route_kernel(
   __shared__ __align__(16) float logits[kMoeMaxExperts];
   __shared__ uint32_t keys[kMoeMaxExperts];
   __shared__ int chosen[kMoeMaxTopK];
-  __shared__ float dots[kRouteWarps];
+  __shared__ float dots[kMoeMaxExperts / 2];  // [expert of the block][part]; 2 blocks at least
   __shared__ unsigned tops[kRouteWarps];
   grid_dependency_wait();  // the call before may still use the workspace, x may not be there yet
   allow_dependent_launch();
   // the first block has to be there before the others write to it: they arrive here and wait
   // just before they do
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  constexpr int kBatch = kXBf16 && kRBf16 ? 8 : 4;  // vectors in flight per lane
   const int t = blockIdx.x / blocks, part = blockIdx.x % blocks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = blockIdx.x * kRouteThreads + threadIdx.x; i < n_clear; i += gridDim.x * kRouteThreads) clear[i] = 0;
   const char* xr = static_cast<const char*>(x) + row_offset(t, D, kXBf16);
-  // `share` warps (a power of two) to an expert, experts part, part + 8, ... of the token
+  // `share` warps (a power of two) to an expert, experts part, part + blocks, ... of the token
   const int experts = max(1, (E - part + blocks - 1) / blocks);  // one that is not there at least
   int share = 1;
-  while (2 * share * experts <= kRouteWarps) share *= 2;
+  while (2 * share * ((E + 7) / 8) <= kRouteWarps) share *= 2;
+  // of the block's experts this warp has number group, group + groups, ...: `mine` of them
+  const int group = warp / share, groups = kRouteWarps / share, mine = (experts - group + groups - 1) / groups;
+  const int stride = 32 * share, first = (warp % share) * 32 + lane;  // of the lane's vectors
+  const int steps = (D / 8 + stride - 1) / stride;
   unsigned m = 0u;  // bits of the largest |x|; those of a NaN are larger still
-  bool met = false;
-  for (int i0 = 0; i0 < experts; i0 += kRouteWarps / share) {
-    const int want = part + blocks * (i0 + warp / share), e = min(want, E - 1);
-    const char* rr = static_cast<const char*>(router) + row_offset(e, D, kRBf16);
-    float s = 0.0f;
-    constexpr int kBatch = kXBf16 && kRBf16 ? 8 : 4;  // vectors in flight per lane
-    for (int c0 = (warp % share) * 32 + lane; c0 < D / 8; c0 += kBatch * 32 * share) {
-      Raw8<kXBf16> a[kBatch];
-      Raw8<kRBf16> b[kBatch];
+  // `kExperts` of the warp's experts at once, `kSteps` vectors of each in flight
+  auto products = [&](auto n_experts, auto n_steps) {
+    constexpr int kExperts = decltype(n_experts)::value, kSteps = decltype(n_steps)::value;
+    for (int i0 = 0; i0 < mine; i0 += kExperts) {
+      const char* rr[kExperts];  // behind the last expert: the last again
+      float s[kExperts];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int c = min(c0 + 32 * share * u, D / 8 - 1);
-        a[u] = load_raw8<kXBf16, true>(xr, c);  // kept in this order: all before the first use
-        b[u] = load_raw8<kRBf16, true>(rr, c);
+      for (int i = 0; i < kExperts; ++i) {
+        const int e = min(part + blocks * (group + groups * min(i0 + i, mine - 1)), E - 1);
+        rr[i] = static_cast<const char*>(router) + row_offset(e, D, kRBf16);
+        s[i] = 0.0f;
       }
+      for (int k = 0; k < steps; k += kSteps) {
+        Raw8<kXBf16> a[kSteps];
+        Raw8<kRBf16> b[kSteps][kExperts];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        float x8[8], r8[8];
-        unpack8<kXBf16>(a[u], x8);
-        unpack8<kRBf16>(b[u], r8);
-        const bool in = c0 + 32 * share * u < D / 8;
+        for (int u = 0; u < kSteps; ++u) {
+          const int c = min(first + stride * (k + u), D / 8 - 1);
+          a[u] = load_raw8<kXBf16, true>(xr, c);  // kept in this order: all before the first use
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          s = fmaf(x8[j], in ? r8[j] : 0.0f, s);
-          m = max(m, __float_as_uint(x8[j]) & 0x7fffffffu);
+          for (int i = 0; i < kExperts; ++i) b[u][i] = load_raw8<kRBf16, true>(rr[i], c);
+        }
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          float x8[8];
+          unpack8<kXBf16>(a[u], x8);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x8[j]) & 0x7fffffffu);
+          const bool in = first + stride * (k + u) < D / 8;
+#pragma unroll
+          for (int i = 0; i < kExperts; ++i) {
+            float r8[8];
+            unpack8<kRBf16>(b[u][i], r8);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[i] = fmaf(x8[j], in ? r8[j] : 0.0f, s[i]);
+          }
         }
       }
+#pragma unroll
+      for (int i = 0; i < kExperts; ++i) {
+        s[i] = warp_sum(s[i]);
+        if (lane == 0 && i0 + i < mine) dots[(group + groups * (i0 + i)) * share + warp % share] = s[i];
+      }
     }
-    s = warp_sum(s);
-    if (share > 1) {
-      __syncthreads();
-      if (lane == 0) dots[warp] = s;
-      __syncthreads();
-      s = 0.0f;
-      for (int j = 0; j < share; ++j) s += dots[warp / share * share + j];
-    }
-    if (!met) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    met = true;
-    if (lane == 0 && warp % share == 0 && want < E) st_cluster_f32(smem_u32(logits + want), 0, s);
-  }
+  };
+  if (mine == 1)
+    products(std::integral_constant<int, 1>{}, std::integral_constant<int, kBatch>{});
+  else  // a row's vectors serve four experts (64 tokens, 512 experts of 4096: 128 -> 111 us, whole layer)
+    products(std::integral_constant<int, 4>{}, std::integral_constant<int, kBatch / 4>{});
   m = __reduce_max_sync(0xffffffffu, m);
   if (lane == 0) tops[warp] = m;
   __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (threadIdx.x < experts && part + blocks * static_cast<int>(threadIdx.x) < E) {
+    float logit = 0.0f;
+    for (int j = 0; j < share; ++j) logit += dots[threadIdx.x * share + j];
+    st_cluster_f32(smem_u32(logits + part + blocks * threadIdx.x), 0, logit);
+  }
   const float a = __uint_as_float(__reduce_max_sync(0xffffffffu, tops[lane % kRouteWarps]));
   const bool fine = a <= kFloatMax;
   if (!fine && threadIdx.x == 0) record_status(kStatusNonfinite);

@@ -248,3 +248,17 @@ def test_norm_then_experts_captured_and_replayed():
             for u, v in zip(out, want[j]):
                 assert torch.equal(u, v)
     assert bl.get_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,D,xtype,rtype", [(8, 3200, BF16, BF16), (64, 4096, BF16, BF16), (3, 16384, BF16, BF16),
+                                             (24, 4096, F32, BF16), (150, 1600, BF16, F32), (512, 4160, BF16, BF16)])
+def test_routing_does_not_depend_on_the_batch(E, D, xtype, rtype):
+    """Rows long enough that a dot product has several terms per lane, on both sides of every change of
+    blocks per token (18 and 19 tokens on 148 SMs): the same logits, so the same fp32 weights and sums."""
+    layer = _layer(E, D, 64, seed=E, rtype=rtype, top_k=min(E, 8), renormalize=False)
+    x = torch.randn((64, D), generator=syn.gen(D)).to(xtype).cuda()
+    y = bl.moe_forward(x, layer, out_dtype=F32)
+    for M in (1, 2, 9, 18, 19, 37):
+        assert torch.equal(bl.moe_forward(x[:M].contiguous(), layer, out_dtype=F32), y[:M]), M
+    assert bl.get_device_status() == 0
