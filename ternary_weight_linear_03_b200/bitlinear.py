@@ -3,6 +3,10 @@
 Argument marshalling only: every step of the BitLinear forward runs in the library's
 sm_100a kernels. PyTorch supplies device memory and the current stream. There is no
 fallback: if the shared library is missing or no CUDA device is present, the calls raise.
+
+stream= runs a call on that stream (of the tensors' device) instead of the current one; what it
+allocates then belongs to that stream. As with any work put on another stream, the caller makes it
+wait for the inputs, keeps them (and buffers it gives) until it is done, and waits for the outputs.
 """
 
 from __future__ import annotations
@@ -159,25 +163,38 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype} (fp32 or bf16)")
 
 
-def _stream(stream) -> int:
+def _stream(stream=None) -> int:
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
+
+
+def _on(stream, fn, *args):
+    """fn(*args) with `stream` as the current one: what fn allocates then belongs to the stream its
+    kernels run on, and not to one that may still use it, or hands it out again once fn has dropped
+    it. New outputs are kept for the caller's stream too."""
+    if args[0].device != stream.device:
+        raise ValueError(f"stream (on {stream.device}) and tensors ({args[0].device}) must be on one device")
+    if stream == torch.cuda.current_stream():
+        return fn(*args)
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = fn(*args)
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None and not any(t is a for a in args):
+            t.record_stream(here)
+    return out
 
 
 # The current stream's handle without a Stream object (3 us less per call), where torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _run(fn, what: str, at: int, stream, *args) -> None:
-    """Calls fn(*args, stream) with device `at` current (on its current stream if none is given)."""
+def _run(fn, what: str, at: int, *args) -> None:
+    """Calls fn(*args, stream) with device `at` current, on its current stream."""
     if at != torch.cuda.current_device():
         with torch.cuda.device(at):
-            return _run(fn, what, at, stream, *args)
-    if stream is None:
-        handle = _raw_stream(at) if _raw_stream is not None else _stream(None)
-    else:
-        handle = stream.cuda_stream
-    status = fn(*args, handle)
+            return _run(fn, what, at, *args)
+    status = fn(*args, _raw_stream(at) if _raw_stream is not None else _stream())
     if status:
         _check(status, what)
 
@@ -231,6 +248,8 @@ def quantize_weights(W: torch.Tensor, eps: float = 1e-5, packed: torch.Tensor | 
                      gamma: torch.Tensor | None = None, ws: torch.Tensor | None = None,
                      stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Absmean ternary quantization of W [N][K] -> (packed uint8 [N][K/4], gamma fp32 [1])."""
+    if stream is not None:
+        return _on(stream, quantize_weights, W, eps, packed, gamma, ws)
     lib = load_library()
     N, K = W.shape
     if packed is None:
@@ -241,19 +260,21 @@ def quantize_weights(W: torch.Tensor, eps: float = 1e-5, packed: torch.Tensor | 
         ws = workspace(1, N, K, W.device)
     _check(lib.bitlinear_quantize_weights(
         _dev(W, "W"), _dtype_code(W), N, K, float(eps), _dev(packed, "packed"),
-        _dev(gamma, "gamma"), _dev(ws, "ws"), ws.numel(), _stream(stream)),
+        _dev(gamma, "gamma"), _dev(ws, "ws"), ws.numel(), _stream()),
         "bitlinear_quantize_weights")
     return packed, gamma
 
 
 def quantize_acts(x: torch.Tensor, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Per-token absmax int8: x [M][K] -> (xq int8 [M][K], scale fp32 [M])."""
+    if stream is not None:
+        return _on(stream, quantize_acts, x)
     lib = load_library()
     M, K = x.shape
     xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
     scale = torch.empty(M, dtype=torch.float32, device=x.device)
     _check(lib.bitlinear_quantize_acts(_dev(x, "x"), _dtype_code(x), M, K, _dev(xq, "xq"),
-                                       _dev(scale, "scale"), _stream(stream)),
+                                       _dev(scale, "scale"), _stream()),
            "bitlinear_quantize_acts")
     return xq, scale
 
@@ -265,6 +286,8 @@ def weight_abssum(W: torch.Tensor, sums: torch.Tensor | None = None,
                   ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Exact sum of |w| over W (a shard of a matrix) as ABSSUM_WORDS int64 words (uint64
     bit patterns): the words of several shards add up exactly to those of their union."""
+    if stream is not None:
+        return _on(stream, weight_abssum, W, sums, ws)
     lib = load_library()
     N, K = W.shape
     if sums is None:
@@ -272,7 +295,7 @@ def weight_abssum(W: torch.Tensor, sums: torch.Tensor | None = None,
     if ws is None:
         ws = workspace(1, N, K, W.device)
     _check(lib.bitlinear_weight_abssum(_dev(W, "W"), _dtype_code(W), N, K, _dev(sums, "sums"),
-                                       _dev(ws, "ws"), ws.numel(), _stream(stream)),
+                                       _dev(ws, "ws"), ws.numel(), _stream()),
            "bitlinear_weight_abssum")
     return sums
 
@@ -283,6 +306,8 @@ def quantize_weights_from_abssum(W: torch.Tensor, n_total: int, sums: torch.Tens
                                  stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """gamma from the added words of every shard (over n_total weights), then this shard's
     packed codes."""
+    if stream is not None:
+        return _on(stream, quantize_weights_from_abssum, W, n_total, sums, eps, packed, gamma)
     lib = load_library()
     N, K = W.shape
     if packed is None:
@@ -291,32 +316,36 @@ def quantize_weights_from_abssum(W: torch.Tensor, n_total: int, sums: torch.Tens
         gamma = torch.empty(1, dtype=torch.float32, device=W.device)
     _check(lib.bitlinear_quantize_weights_from_abssum(
         _dev(W, "W"), _dtype_code(W), N, K, int(n_total), _dev(sums, "sums"), float(eps),
-        _dev(packed, "packed"), _dev(gamma, "gamma"), _stream(stream)),
+        _dev(packed, "packed"), _dev(gamma, "gamma"), _stream()),
         "bitlinear_quantize_weights_from_abssum")
     return packed, gamma
 
 
 def act_absmax(x: torch.Tensor, amax: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Per-token max |x| (fp32 [M])."""
+    if stream is not None:
+        return _on(stream, act_absmax, x, amax)
     lib = load_library()
     M, K = x.shape
     if amax is None:
         amax = torch.empty(M, dtype=torch.float32, device=x.device)
     _check(lib.bitlinear_act_absmax(_dev(x, "x"), _dtype_code(x), M, K, _dev(amax, "amax"),
-                                    _stream(stream)), "bitlinear_act_absmax")
+                                    _stream()), "bitlinear_act_absmax")
     return amax
 
 
 def quantize_acts_absmax(x: torch.Tensor, amax: torch.Tensor,
                          stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Per-token int8 quantization with the absmax given (of the whole rows)."""
+    if stream is not None:
+        return _on(stream, quantize_acts_absmax, x, amax)
     lib = load_library()
     M, K = x.shape
     xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
     scale = torch.empty(M, dtype=torch.float32, device=x.device)
     _check(lib.bitlinear_quantize_acts_absmax(_dev(x, "x"), _dtype_code(x), M, K,
                                               _dev(amax, "amax"), _dev(xq, "xq"),
-                                              _dev(scale, "scale"), _stream(stream)),
+                                              _dev(scale, "scale"), _stream()),
            "bitlinear_quantize_acts_absmax")
     return xq, scale
 
@@ -325,12 +354,14 @@ def rescale(acc: torch.Tensor, scale: torch.Tensor, gamma: torch.Tensor,
             out_dtype: torch.dtype = torch.bfloat16, y: torch.Tensor | None = None,
             stream=None) -> torch.Tensor:
     """y = float(acc) * (scale_t * gamma) for an int32 product [M][N]."""
+    if stream is not None:
+        return _on(stream, rescale, acc, scale, gamma, out_dtype, y)
     lib = load_library()
     M, N = acc.shape
     if y is None:
         y = torch.empty((M, N), dtype=out_dtype, device=acc.device)
     _check(lib.bitlinear_rescale(_dev(acc, "acc"), _dev(scale, "scale"), _dev(gamma, "gamma"),
-                                 _dev(y, "y"), _dtype_code(y), M, N, _stream(stream)),
+                                 _dev(y, "y"), _dtype_code(y), M, N, _stream()),
            "bitlinear_rescale")
     return y
 
@@ -360,6 +391,8 @@ def chain_forward(x: torch.Tensor, layers, out_dtype: torch.dtype = torch.bfloat
                   stream=None) -> torch.Tensor:
     """A chain of BitLinear layers (bitlinear_chain_forward): layers are (packed, gamma,
     src[, out]) with src = -1 for x or the index of the layer whose output is the input."""
+    if stream is not None:
+        return _on(stream, chain_forward, x, layers, out_dtype, y, ws)
     lib = load_library()
     M = x.shape[0]
     arr = chain_layers(layers)
@@ -369,7 +402,7 @@ def chain_forward(x: torch.Tensor, layers, out_dtype: torch.dtype = torch.bfloat
         ws = chain_workspace(M, layers, x.device)
     _check(lib.bitlinear_chain_forward(_dev(x, "x"), _dtype_code(x), M, arr, len(layers),
                                        _dev(y, "y"), _dtype_code(y), _dev(ws, "ws"), ws.numel(),
-                                       _stream(stream)), "bitlinear_chain_forward")
+                                       _stream()), "bitlinear_chain_forward")
     return y
 
 
@@ -379,11 +412,13 @@ def base3_row_bytes(K: int) -> int:
 
 def pack_base3(packed: torch.Tensor, stream=None) -> torch.Tensor:
     """2-bit packed weights [N][K/4] -> base-3 [N][ceil(K/80)*16] (same codes)."""
+    if stream is not None:
+        return _on(stream, pack_base3, packed)
     lib = load_library()
     N, K = packed.shape[0], packed.shape[1] * 4
     out = torch.empty((N, base3_row_bytes(K)), dtype=torch.uint8, device=packed.device)
     _check(lib.bitlinear_pack_base3(_dev(packed, "packed"), N, K, _dev(out, "packed3"),
-                                    _stream(stream)), "bitlinear_pack_base3")
+                                    _stream()), "bitlinear_pack_base3")
     return out
 
 
@@ -391,6 +426,8 @@ def forward_base3(x: torch.Tensor, packed3: torch.Tensor, gamma: torch.Tensor,
                   out_dtype: torch.dtype = torch.bfloat16, y: torch.Tensor | None = None,
                   stream=None) -> torch.Tensor:
     """BitLinear forward on base-3 weights (M <= 4 tokens)."""
+    if stream is not None:
+        return _on(stream, forward_base3, x, packed3, gamma, out_dtype, y)
     lib = load_library()
     M, K = x.shape
     N = packed3.shape[0]
@@ -400,17 +437,19 @@ def forward_base3(x: torch.Tensor, packed3: torch.Tensor, gamma: torch.Tensor,
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
     _check(lib.bitlinear_forward_base3(
         _dev(x, "x"), _dtype_code(x), _dev(packed3, "packed3"), _dev(gamma, "gamma"),
-        _dev(y, "y"), _dtype_code(y), M, N, K, _stream(stream)), "bitlinear_forward_base3")
+        _dev(y, "y"), _dtype_code(y), M, N, K, _stream()), "bitlinear_forward_base3")
     return y
 
 
 def pack_transpose(packed: torch.Tensor, stream=None) -> torch.Tensor:
     """2-bit weights [N][K/4] -> the transposed 2-bit weights [K][N/4] (N % 64 == 0)."""
+    if stream is not None:
+        return _on(stream, pack_transpose, packed)
     lib = load_library()
     N, K = packed.shape[0], packed.shape[1] * 4
     out = torch.empty((K, N // 4), dtype=torch.uint8, device=packed.device)
     _check(lib.bitlinear_pack_transpose(_dev(packed, "packed"), N, K, _dev(out, "packedT"),
-                                        _stream(stream)), "bitlinear_pack_transpose")
+                                        _stream()), "bitlinear_pack_transpose")
     return out
 
 
@@ -419,6 +458,8 @@ def backward(x: torch.Tensor, grad_y: torch.Tensor, packedT: torch.Tensor, gamma
              stream=None):
     """Straight-through BitLinear backward: (grad_x fp32 [M][K] or None, grad_w fp32 [N][K]
     or None) from the forward input x, grad_y bf16 [M][N] and the transposed weights."""
+    if stream is not None:
+        return _on(stream, backward, x, grad_y, packedT, gamma, need_x, need_w, ws)
     lib = load_library()
     M, K = x.shape
     N = grad_y.shape[1]
@@ -436,7 +477,7 @@ def backward(x: torch.Tensor, grad_y: torch.Tensor, packedT: torch.Tensor, gamma
         _dev(gamma, "gamma"), _dev(gx, "grad_x") if gx is not None else None,
         _dev(gw, "grad_w") if gw is not None else None, M, N, K,
         _dev(ws, "ws") if ws is not None else None, ws.numel() if ws is not None else 0,
-        _stream(stream)), "bitlinear_backward")
+        _stream()), "bitlinear_backward")
     return gx, gw
 
 
@@ -454,12 +495,15 @@ def backward_quantized(xq: torch.Tensor, scale: torch.Tensor, grad_y: torch.Tens
                        packedT: torch.Tensor, gamma: torch.Tensor, need_x: bool = True,
                        need_w: bool = True, ws: torch.Tensor | None = None, stream=None):
     """backward for a forward that ran on int8 activations xq [M][K] with scales [M]."""
+    if stream is not None:
+        return _on(stream, backward_quantized, xq, scale, grad_y, packedT, gamma, need_x, need_w,
+                   ws)
     (M, K), N, at = xq.shape, grad_y.shape[1], _index(xq, "xq")
     gx = scale.new_empty((M, K)) if need_x else None
     gw = scale.new_empty((N, K)) if need_w else None
     if ws is None:
         ws = backward_workspace(M, N, K, xq.device)
-    _run((_lib or load_library()).bitlinear_backward_quantized, "bitlinear_backward_quantized", at, stream,
+    _run((_lib or load_library()).bitlinear_backward_quantized, "bitlinear_backward_quantized", at,
          _take(xq, "xq", (M, K), torch.int8, at), _take(scale, "scale", (M,), torch.float32, at),
          _take(grad_y, "grad_y", (M, N), torch.bfloat16, at),
          _take(packedT, "packedT", (K, N // 4), torch.uint8, at),
@@ -475,12 +519,14 @@ def forward_quantized(xq: torch.Tensor, scale: torch.Tensor, packed: torch.Tenso
                       stream=None) -> torch.Tensor:
     """BitLinear forward of int8 activations xq [M][K] with scales [M] (rmsnorm_quantize,
     quantize_acts): y [M][N]."""
+    if stream is not None:
+        return _on(stream, forward_quantized, xq, scale, packed, gamma, out_dtype, y, ws)
     (M, K), N, at = xq.shape, packed.shape[0], _index(xq, "xq")
     if y is None:
         y = xq.new_empty((M, N), dtype=out_dtype)
     if ws is None and (M > FEW_TOKENS or K > 32768):
         ws = workspace(M, N, K, xq.device)
-    _run((_lib or load_library()).bitlinear_forward_quantized, "bitlinear_forward_quantized", at, stream,
+    _run((_lib or load_library()).bitlinear_forward_quantized, "bitlinear_forward_quantized", at,
          _take(xq, "xq", (M, K), torch.int8, at), _take(scale, "scale", (M,), torch.float32, at),
          _take(packed, "packed", (N, K // 4), torch.uint8, at),
          _take(gamma, "gamma", (1,), torch.float32, at), _take(y, "y", (M, N), _FLOATS, at),
@@ -499,6 +545,8 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
     """RMS norm of h = x + residual with gain weight [K], as int8 codes: (xq [M][K], scale [M],
     h [M][K], rstd [M]). h is x itself without a residual; it may be given as x or residual
     (added in place). normed, if given, receives the normalised rows themselves."""
+    if stream is not None:
+        return _on(stream, rmsnorm_quantize, x, weight, residual, eps, h, xq, scale, rstd, normed)
     (M, K), at, dt = x.shape, _index(x, "x"), x.dtype
     if residual is None:
         h = x
@@ -511,7 +559,7 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
     if rstd is None:
         rstd = x.new_empty(M, dtype=torch.float32)
     row = (M,)
-    _run((_lib or load_library()).bitlinear_rmsnorm_quantize, "bitlinear_rmsnorm_quantize", at, stream,
+    _run((_lib or load_library()).bitlinear_rmsnorm_quantize, "bitlinear_rmsnorm_quantize", at,
          _take(x, "x", (M, K), _FLOATS, at),
          None if residual is None else _take(residual, "residual", (M, K), dt, at), _code(x),
          _take(weight, "weight", (K,), _FLOATS, at), _code(weight), eps, M, K,
@@ -541,6 +589,9 @@ def rmsnorm_backward(grad_n: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
     the residual alike, grad_weight fp32 [K]) from the gradient grad_n of the normalised rows
     and, if given, the gradient grad_h that reaches h past the norm (of grad_x's type; grad_x
     may be grad_h itself)."""
+    if stream is not None:
+        return _on(stream, rmsnorm_backward, grad_n, h, weight, rstd, grad_h, out_dtype, grad_x,
+                   grad_weight, ws)
     (M, K), at = h.shape, _index(h, "h")
     if grad_x is None:
         grad_x = h.new_empty((M, K), dtype=out_dtype)
@@ -548,7 +599,7 @@ def rmsnorm_backward(grad_n: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
         grad_weight = h.new_empty(K, dtype=torch.float32)
     if ws is None:
         ws = rmsnorm_backward_workspace(M, K, h.device)
-    _run((_lib or load_library()).bitlinear_rmsnorm_backward, "bitlinear_rmsnorm_backward", at, stream,
+    _run((_lib or load_library()).bitlinear_rmsnorm_backward, "bitlinear_rmsnorm_backward", at,
          _take(grad_n, "grad_n", (M, K), _FLOATS, at), _code(grad_n), _take(h, "h", (M, K), _FLOATS, at),
          _code(h), _take(weight, "weight", (K,), _FLOATS, at), _code(weight),
          _take(rstd, "rstd", (M,), torch.float32, at),
@@ -564,13 +615,15 @@ ACTIVATIONS = {"silu": 0, "relu2": 1}
 def quantize_expert_weights(W: torch.Tensor, eps: float = 1e-5,
                             stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """quantize_weights of every expert of W [E][N][K] -> (packed [E][N][K/4], gamma [E])."""
+    if stream is not None:
+        return _on(stream, quantize_expert_weights, W, eps)
     E, N, K = W.shape
     packed = torch.empty((E, N, K // 4), dtype=torch.uint8, device=W.device)
     one = torch.empty((E, 4), dtype=torch.float32, device=W.device)  # each gamma 16-byte aligned
     ws = workspace(1, N, K, W.device)
-    with torch.cuda.device(W.device), torch.cuda.stream(stream):
+    with torch.cuda.device(W.device):
         for e in range(E):
-            quantize_weights(W[e], eps, packed[e], one[e, :1], ws, stream)
+            quantize_weights(W[e], eps, packed[e], one[e, :1], ws)
         return packed, one[:, 0].contiguous()
 
 
@@ -612,12 +665,14 @@ def moe_forward(x: torch.Tensor, layer: MoeLayer, out_dtype: torch.dtype = torch
                 y: torch.Tensor | None = None, ws: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
     """A mixture-of-experts layer for a few tokens (up to 64): x [M][D] -> y [M][D]."""
+    if stream is not None:
+        return _on(stream, moe_forward, x, layer, out_dtype, y, ws)
     M, at, shape = x.shape[0], _index(layer.tensors[0], "router"), (x.shape[0], layer.D)
     if y is None:
         y = layer.tensors[0].new_empty(shape, dtype=out_dtype)
     if ws is None:
         ws = moe_workspace(M, layer)
-    _run((_lib or load_library()).bitlinear_moe_forward, "bitlinear_moe_forward", at, stream,
+    _run((_lib or load_library()).bitlinear_moe_forward, "bitlinear_moe_forward", at,
          _take(x, "x", shape, _FLOATS, at), _code(x), M, layer._ref, _take(y, "y", shape, _FLOATS, at), _code(y),
          _take_ws(ws, at), ws.numel())
     return y
@@ -627,6 +682,8 @@ def forward(x: torch.Tensor, packed: torch.Tensor, gamma: torch.Tensor,
             out_dtype: torch.dtype = torch.bfloat16, y: torch.Tensor | None = None,
             ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """BitLinear forward: y [M][N] = rescale(int32 contraction of quantized x with W)."""
+    if stream is not None:
+        return _on(stream, forward, x, packed, gamma, out_dtype, y, ws)
     lib = load_library()
     M, K = x.shape
     N = packed.shape[0]
@@ -638,7 +695,7 @@ def forward(x: torch.Tensor, packed: torch.Tensor, gamma: torch.Tensor,
         ws = workspace(M, N, K, x.device)
     _check(lib.bitlinear_forward(
         _dev(x, "x"), _dtype_code(x), _dev(packed, "packed"), _dev(gamma, "gamma"), _dev(y, "y"),
-        _dtype_code(y), M, N, K, _dev(ws, "ws"), ws.numel(), _stream(stream)),
+        _dtype_code(y), M, N, K, _dev(ws, "ws"), ws.numel(), _stream()),
         "bitlinear_forward")
     return y
 
@@ -649,6 +706,8 @@ def forward_noalloc(x: torch.Tensor, packed: torch.Tensor, gamma: torch.Tensor,
     """bitlinear_forward without a workspace: the library's built-in 16 MiB device scratch
     serves the tensor-core path (for callers that cannot allocate; calls must not overlap
     on the GPU)."""
+    if stream is not None:
+        return _on(stream, forward_noalloc, x, packed, gamma, out_dtype, y)
     lib = load_library()
     M, K = x.shape
     N = packed.shape[0]
@@ -658,13 +717,15 @@ def forward_noalloc(x: torch.Tensor, packed: torch.Tensor, gamma: torch.Tensor,
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
     _check(lib.bitlinear_forward_noalloc(
         _dev(x, "x"), _dtype_code(x), _dev(packed, "packed"), _dev(gamma, "gamma"), _dev(y, "y"),
-        _dtype_code(y), M, N, K, _stream(stream)), "bitlinear_forward_noalloc")
+        _dtype_code(y), M, N, K, _stream()), "bitlinear_forward_noalloc")
     return y
 
 
 def contract_i32(xq: torch.Tensor, packed: torch.Tensor, acc: torch.Tensor | None = None,
                  ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Integer stage only: acc [M][N] int32 = sum_k c[n,k] * xq[t,k]."""
+    if stream is not None:
+        return _on(stream, contract_i32, xq, packed, acc, ws)
     lib = load_library()
     M, K = xq.shape
     N = packed.shape[0]
@@ -673,7 +734,7 @@ def contract_i32(xq: torch.Tensor, packed: torch.Tensor, acc: torch.Tensor | Non
     if ws is None:
         ws = workspace(M, N, K, xq.device)
     _check(lib.bitlinear_contract_i32(_dev(xq, "xq"), _dev(packed, "packed"), _dev(acc, "acc"),
-                                      M, N, K, _dev(ws, "ws"), ws.numel(), _stream(stream)),
+                                      M, N, K, _dev(ws, "ws"), ws.numel(), _stream()),
            "bitlinear_contract_i32")
     return acc
 
