@@ -156,11 +156,13 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_quant_kernel(
       float p[8], g[8];
       unpack8<kBf16>(hv[v], p);
       load8<kWBf16>(w, c, g);
+      float part = 0.0f;  // a thread adds sums of 8, not all of its 8 V squares in one row
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        ss = fmaf(p[i], p[i], ss);
+        part = fmaf(p[i], p[i], part);
         m = max_nan(m, fabsf(__fmul_rn(p[i], g[i])));  // a NaN of the gain is in p alone
       }
+      ss = __fadd_rn(ss, part);
     }
   }
   ss = warp_sum(ss);

@@ -250,3 +250,20 @@ def test_norm_reports_nonfinite_gains(bad, under, K, wtype):
         assert bl.get_device_status() == 6
         bl.rmsnorm_quantize(x.cuda(), torch.ones(K, dtype=wtype).cuda())
         assert bl.get_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K,dtype", [(28672, BF16), (20480, BF16), (32768, F32), (3200, F32), (1536, BF16)])
+@pytest.mark.parametrize("every", [8, 16, 64])
+def test_norm_statistics_of_squares_lost_one_by_one(K, dtype, every):
+    """A large square followed by many of just under half its last place: a running sum drops each of them
+    whole, which for 64 in a row is 31 u of rstd, beyond the 28 u stated above."""
+    x = torch.full((200, K), 2.0 ** -12 * (1 - 2.0 ** -8), dtype=dtype)
+    nv = K // 8
+    ones = nv // (every // 8)
+    x[:, : 8 * ones : 8] = 1.0
+    _, scale, _, rstd = bl.rmsnorm_quantize(x.cuda(), torch.ones(K).cuda(), eps=1e-10)
+    assert bl.get_device_status() == 0
+    rs = 1.0 / (x.double().square().mean(-1) + 1e-10).sqrt()
+    assert ((rstd.cpu().double() - rs).abs() <= 28 * U * rs).all()
+    assert ((scale.cpu().double() - rs / 127).abs() <= 30 * U * rs / 127).all()
