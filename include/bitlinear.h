@@ -250,8 +250,10 @@ size_t bitlinear_moe_workspace_size(int M, const bl_moe* layer);
  *   x      device, [M][D], fp32 or bf16.   y  device, [M][D], BL_F32 or BL_BF16.
  *   layer  host pointer, read before the call returns.
  *   ws     device, bitlinear_moe_workspace_size(M, layer) bytes (contents ignored).
- * 1 <= M <= 64; E <= 512; top_k <= min(E, 16); D, F multiples of 64, up to 16384; else BL_ERR_UNSUPPORTED_SHAPE. Inf/NaN in x, or logits that are not
- * finite, set BL_ERR_NONFINITE in the status word. */
+ * 1 <= M <= 64; E <= 512; top_k <= min(E, 16); D, F multiples of 64, up to 16384; else
+ * BL_ERR_UNSUPPORTED_SHAPE. Inf/NaN in x, logits that are not finite, or an act(G) * U that is not
+ * (one that passes fp32, a gamma that is NaN) set BL_ERR_NONFINITE in the status word. A token's
+ * outputs have the same bits whatever other tokens the call has. */
 bl_status bitlinear_moe_forward(const void* x, int x_dtype, int M, const bl_moe* layer, void* y,
                                 int y_dtype, void* ws, size_t ws_bytes, void* stream);
 

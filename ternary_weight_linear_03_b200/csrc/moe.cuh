@@ -22,7 +22,7 @@ enum MoeAct : int { kActSilu = 0, kActRelu2 = 1 };
 
 __device__ __forceinline__ float moe_act(float g, int act) {
   if (act == kActSilu) return __fdiv_rn(g, __fadd_rn(1.0f, expf(-g)));
-  const float r = fmaxf(g, 0.0f);
+  const float r = max_nan(g, 0.0f);
   return __fmul_rn(r, r);
 }
 

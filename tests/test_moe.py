@@ -262,3 +262,17 @@ def test_routing_does_not_depend_on_the_batch(E, D, xtype, rtype):
     for M in (1, 2, 9, 18, 19, 37):
         assert torch.equal(bl.moe_forward(x[:M].contiguous(), layer, out_dtype=F32), y[:M]), M
     assert bl.get_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "relu2"])
+@pytest.mark.parametrize("which,bad", [("gate", float("nan")), ("up", float("nan")), ("gate", 1e38), ("up", 1e38)])
+def test_nonfinite_inner_rows_are_reported(act, which, bad):
+    """An activation times the other factor that is NaN or passes fp32 in one chosen expert, in either place."""
+    layer = _layer(4, 128, 64, seed=1, top_k=4, activation=act)
+    x = 100 * torch.randn((3, 128), generator=syn.gen(3)).cuda()
+    bl.moe_forward(x, layer)
+    assert bl.get_device_status() == 0
+    layer.tensors[4 if which == "gate" else 5][2] = bad
+    bl.moe_forward(x, layer)
+    assert bl.get_device_status() == 6
