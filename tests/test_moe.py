@@ -276,3 +276,110 @@ def test_nonfinite_inner_rows_are_reported(act, which, bad):
     layer.tensors[4 if which == "gate" else 5][2] = bad
     bl.moe_forward(x, layer)
     assert bl.get_device_status() == 6
+
+
+def _random_layer(E, D, F, seed, **kw):
+    """Random trits and, for each token, a random order of the experts with gaps between the logits: the
+    router picks x[t, :E] out, which holds a permutation of whole 32nds."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def stack(N, K):
+        u = torch.randint(0, 3, (4, E, N, K // 4), generator=g, device="cuda", dtype=torch.uint8)
+        return u[0] | u[1] << 2 | u[2] << 4 | u[3] << 6, 0.01 + 0.02 * torch.rand(E, generator=g, device="cuda")
+
+    router = torch.zeros((E, D), device="cuda")
+    router[torch.arange(E), torch.arange(E)] = 0.5
+    return bl.MoeLayer(router.bfloat16(), *stack(F, D), *stack(F, D), *stack(D, F), **kw)
+
+
+def _random_tokens(M, E, D, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((M, D), generator=g, device="cuda")
+    x[:, :E] = torch.rand((M, E), generator=g, device="cuda").argsort(-1) / 32.0
+    return x.bfloat16()
+
+
+def _trits64(packed):
+    """2-bit codes [N, K/4] -> trits [N, K] in 64 bits."""
+    b = packed.to(torch.int32).unflatten(-1, (-1, 4))
+    return torch.stack([(b >> 2 * j) & 3 for j in range(4)], -2).flatten(-3).double() - 1
+
+
+def _codes64(v):
+    """_quantize on the GPU."""
+    a = v.abs().amax(-1)
+    f = torch.where(a > 0, torch.full_like(a, 127).float() / a.float(), torch.zeros_like(a).float()).double()
+    t = v * f[:, None]
+    return t.float().double().round().clamp(-127, 127), a / 127, t
+
+
+def _reference_by_expert(x, layer, act, renorm):
+    """_reference, expert by expert on the GPU: (y, bound on the error before y's own rounding)."""
+    router, gate, up, down, gg, ug, dg = layer.tensors
+    E, k = layer.E, layer.top_k
+    xd = x.double()
+    logits = xd @ router.double().T
+    dl = ((layer.D / 32 + 16) * U * (xd.abs() @ router.double().abs().T)).amax(1)
+    order = logits.argsort(dim=-1, descending=True, stable=True)
+    if k < E:
+        ranked = logits.gather(1, order)
+        assert (ranked[:, k - 1] - ranked[:, k] > 2 * dl).all()
+    e = torch.exp(logits - logits.amax(1, keepdim=True))
+    chosen = torch.zeros_like(e, dtype=torch.bool).scatter_(1, order[:, :k], True)
+    w = e / ((e * chosen).sum(1, keepdim=True) if renorm else e.sum(1, keepdim=True))
+    q, s, _ = _codes64(xd)
+    y, tol = torch.zeros_like(xd), torch.zeros_like(xd)
+    for j in range(E):
+        t = chosen[:, j].nonzero()[:, 0]
+        if not len(t):
+            continue
+        cd = _trits64(down[j])
+        G = (q[t] @ _trits64(gate[j]).T) * s[t, None] * gg[j].double()
+        Uv = (q[t] @ _trits64(up[j]).T) * s[t, None] * ug[j].double()
+        inner = (G / (1 + torch.exp(-G)) if act == "silu" else G.clamp(min=0).square()) * Uv
+        rel = (16 + 4 * G.abs()) * U
+        hq, hs, scaled = _codes64(inner)
+        worst = rel.gather(1, inner.abs().argmax(1, keepdim=True)) + 4 * U
+        near = ((scaled - scaled.floor()).abs() - 0.5).abs() <= scaled.abs() * (rel + worst) + 1e-12
+        o = (hq @ cd.T) * (hs * dg[j].double())[:, None]
+        flips = (near.double() @ cd.abs().T) * (hs * dg[j].double())[:, None]
+        wrel = 2 * dl[t, None] + (E + 16) * U
+        wt = w[t, j, None]
+        y[t] += wt * o
+        tol[t] += wt * (flips + o.abs() * (worst + wrel + 4 * U)) + k * U * (wt * o).abs()
+    return y, tol
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,E,D,F,top_k,act", [
+    # 16 columns: several turns of all warps over both widths, several groups of an expert's tokens
+    (24, 2, 4224, 8320, 1, "silu"), (40, 3, 4224, 4544, 2, "relu2"),
+    # up to 4 and up to 8 tokens, rows wider than a turn
+    (3, 2, 8320, 9024, 1, "silu"), (7, 2, 8320, 8960, 2, "relu2"),
+    # stretches of a block that end a run at its limit and go on in the same expert: 8 columns, gate and
+    # up / down; 16 columns, gate and up / down
+    (64, 128, 512, 1536, 8, "silu"), (64, 128, 4096, 64, 8, "silu"),
+    (64, 8, 192, 8640, 2, "silu"), (64, 8, 16384, 64, 2, "relu2"),
+])
+def test_moe_of_wide_rows_and_long_stretches(M, E, D, F, top_k, act):
+    layer = _random_layer(E, D, F, seed=D + F, top_k=top_k, activation=act)
+    x = _random_tokens(M, E, D, seed=M)
+    y = bl.moe_forward(x, layer, out_dtype=F32)
+    assert bl.get_device_status() == 0
+    ref, tol = _reference_by_expert(x, layer, act, True)
+    err = (y.double() - ref).abs()
+    tol = tol * (1 + 2.0 ** -7) + U * ref.abs() + 1e-30
+    assert (err <= tol).all(), float((err / tol).max())
+    y16 = bl.moe_forward(x, layer)
+    assert torch.equal(y16, y.bfloat16())
+
+
+@pytest.mark.gpu
+def test_the_two_references_agree():
+    """The reference by expert against the one by token, on a layer that both can take."""
+    layer = _random_layer(6, 128, 192, seed=1, top_k=2)
+    x = _random_tokens(5, 6, 128, seed=2)
+    a, ta = _reference(x.cpu(), layer, "silu", True)
+    b, tb = _reference_by_expert(x, layer, "silu", True)
+    np.testing.assert_allclose(b.cpu().numpy(), a, rtol=1e-12, atol=1e-13)
+    np.testing.assert_allclose(tb.cpu().numpy(), ta, rtol=1e-9, atol=1e-13)
