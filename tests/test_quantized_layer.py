@@ -194,3 +194,76 @@ def test_captured_and_on_another_stream():
         static.copy_(x)
         graph.replay()
         assert torch.equal(y, a) and torch.equal(h, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(1, 64, 64), (77, 640, 320), (700, 128, 192)])
+def test_each_gradient_alone(M, N, K):
+    """One gradient without the other: the same bits, and the other's operands are not needed."""
+    q, s = _codes(M, K, M)
+    G = (torch.randn((M, N), generator=syn.gen(M)) * 0.01).bfloat16().cuda()
+    packed, gamma = bl.quantize_weights(syn.weights(N, K, 0.02, seed=2).cuda())
+    args = q.cuda(), s.cuda(), G, bl.pack_transpose(packed), gamma
+    gx, gw = bl.backward_quantized(*args)
+    none, only_w = bl.backward_quantized(*args, need_x=False)
+    assert none is None and torch.equal(only_w, gw)
+    only_x, none = bl.backward_quantized(*args, need_w=False)
+    assert none is None and torch.equal(only_x, gx)
+    ws, stream = bl.backward_workspace(M, N, K), torch.cuda.current_stream().cuda_stream
+    again = torch.full_like(gw, float("nan"))
+    assert bl.load_library().bitlinear_backward_quantized(
+        args[0].data_ptr(), args[1].data_ptr(), G.data_ptr(), None, None, None, again.data_ptr(), M, N, K,
+        ws.data_ptr(), ws.numel(), stream) == 0
+    assert torch.equal(again, gw)
+    again = torch.full_like(gx, float("nan"))
+    assert bl.load_library().bitlinear_backward_quantized(
+        None, None, G.data_ptr(), args[3].data_ptr(), gamma.data_ptr(), again.data_ptr(), None, M, N, K,
+        ws.data_ptr(), ws.numel(), stream) == 0
+    assert torch.equal(again, gx)
+
+
+# A contraction of n terms runs in parts of 512: 32 matrix instructions of 16 terms each, and one fp32
+# addition per part. The tensor core truncates: at each instruction the accumulator and the 16 products
+# are cut at the place of the largest, two places (2^-23 of the sum so far) at most in all; over the
+# 2063 instructions of one accumulator below that is 2.4e-4, of which 1.8e-4 is measured.
+def _split_bound(n, mag):
+    return (2 * min(-(-n // 16), 32) * 2.0 ** -23 + -(-n // 512) * 2.0 ** -24) * mag
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [500, 4096, 33000])
+@pytest.mark.parametrize("side", ["tokens", "outputs"])
+def test_long_sums_of_one_sign_are_taken_in_parts(n, side):
+    """Terms of one sign, where truncation errors add up: one accumulator for all of 33000 terms is
+    off by 1.8e-4 (bitlinear_backward's, measured), parts of 512 by the bound's 1.2e-5 at most."""
+    n = -(-n // 64) * 64 if side == "outputs" else n
+    M, N, K = (n, 64, 64) if side == "tokens" else (40, n, 64)
+    q = torch.randint(64, 128, (M, K), generator=syn.gen(1)).to(torch.int8)
+    s = 0.5 + torch.rand(M, generator=syn.gen(2))
+    G = (0.5 + torch.rand((M, N), generator=syn.gen(3))).bfloat16()
+    packed, gamma = bl.quantize_weights(torch.ones((N, K)).cuda())
+    gx, gw = bl.backward_quantized(q.cuda(), s.cuda(), G.cuda(), bl.pack_transpose(packed), gamma)
+    if side == "tokens":
+        got, ref = gw, G.double().T @ (q.float() * s[:, None]).bfloat16().double()
+    else:
+        got, ref = gx, (float(gamma.item()) * G.double().sum(1, keepdim=True)).expand(M, K)
+    err = (got.cpu().double() - ref).abs()
+    bound = _split_bound(n, ref) + 2.0 ** -23 * ref
+    assert (err <= bound).all(), float((err / bound).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(1, 64, 64), (130, 640, 1536), (1025, 128, 192), (2600, 192, 64), (33, 2112, 64)])
+def test_gradients_within_the_bound_of_their_parts(M, N, K):
+    """As test_backward_matches_oracle, with a bound that does not grow with the length: a token
+    left out or counted twice among 2600 exceeds it."""
+    q, s = _codes(M, K, M + N + K)
+    G = (torch.randn((M, N), generator=syn.gen(M)) * 0.01).bfloat16()
+    packed, gamma = bl.quantize_weights(syn.weights(N, K, 0.02, seed=2).cuda())
+    gx, gw = bl.backward_quantized(q.cuda(), s.cuda(), G.cuda(), bl.pack_transpose(packed), gamma)
+    codes = torch.from_numpy(orc.unpack(packed.cpu().numpy(), K)).double()
+    g, xt = float(gamma.item()), (q.float() * s[:, None]).bfloat16().double()
+    for got, ref, mag, n in ((gx, g * (G.double() @ codes), g * (G.double().abs() @ codes.abs()), N),
+                             (gw, G.double().T @ xt, G.double().abs().T @ xt.abs(), M)):
+        err = (got.cpu().double() - ref).abs()
+        assert (err <= _split_bound(n, mag) + 2.0 ** -23 * ref.abs()).all()
