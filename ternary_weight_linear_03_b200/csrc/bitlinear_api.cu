@@ -903,19 +903,6 @@ int grid_for(long long work, int per_block) {
       1, std::min<long long>((work + per_block - 1) / per_block, 16ll * num_sms())));
 }
 
-// grad_w = G^T X~ from the int8 codes and scales: both operands transposed into the
-// workspace, then the contraction over the tokens.
-bl_status launch_grad_w(const int8_t* xq, const float* scale, const void* grad_y, float* grad_w,
-                        int M, int N, int K, const BwdWs& w, cudaStream_t s) {
-  const int tiles_g = ((w.Mp + 63) / 64) * (N / 64);
-  bl::transpose_bf16_kernel<0><<<grid_for(tiles_g, 1), 256, 0, s>>>(grad_y, nullptr, w.gT, M, N,
-                                                                     w.Mp);
-  const int tiles_x = ((w.Mp + 63) / 64) * (K / 64);
-  bl::transpose_bf16_kernel<1><<<grid_for(tiles_x, 1), 256, 0, s>>>(xq, scale, w.xT, M, K, w.Mp);
-  if (launch_status() != BL_OK) return BL_ERR_CUDA;
-  return launch_gemm_bf16<false>(w.gT, w.xT, nullptr, grad_w, N, K, w.Mp, s);
-}
-
 }  // namespace
 
 extern "C" {
@@ -955,7 +942,14 @@ bl_status bitlinear_backward(const void* x, int x_dtype, const void* grad_y,
     if (ws_bytes < w.bytes) return BL_ERR_WORKSPACE;
     bl_status st = launch_act_quant(x, x_dtype, M, K, w.f.xq, w.f.scale, nullptr, s);
     if (st != BL_OK) return st;
-    st = launch_grad_w(w.f.xq, w.f.scale, grad_y, grad_w, M, N, K, w, s);
+    const int tiles_g = ((w.Mp + 63) / 64) * (N / 64);
+    bl::transpose_bf16_kernel<0><<<grid_for(tiles_g, 1), 256, 0, s>>>(grad_y, nullptr, w.gT, M,
+                                                                       N, w.Mp);
+    const int tiles_x = ((w.Mp + 63) / 64) * (K / 64);
+    bl::transpose_bf16_kernel<1><<<grid_for(tiles_x, 1), 256, 0, s>>>(w.f.xq, w.f.scale, w.xT,
+                                                                       M, K, w.Mp);
+    if (launch_status() != BL_OK) return BL_ERR_CUDA;
+    st = launch_gemm_bf16<false>(w.gT, w.xT, nullptr, grad_w, N, K, w.Mp, s);
     if (st != BL_OK) return st;
   }
   if (grad_x) return launch_gemm_bf16<true>(grad_y, packedT, gamma, grad_x, M, K, N, s);
@@ -1577,7 +1571,6 @@ bl_status bitlinear_moe_forward(const void* x, int x_dtype, int M, const bl_moe*
   if (st != BL_OK) return st;
   bl::MoeArgs a{};
   a.ids = w.ids;
-  a.weights = w.weights;
   a.xq = w.xq;
   a.xscale = w.scale;
   a.gate = m.gate;

@@ -266,7 +266,6 @@ __device__ __forceinline__ void moe_group(MoeGroups& g, const int* ids, int pair
 // Everything that the two expert kernels read and write.
 struct MoeArgs {
   const int* ids;         // [pairs]
-  const float* weights;   // [pairs]
   const int8_t* xq;       // [M][D]
   const float* xscale;    // [M]
   const uint8_t *gate, *up, *down;
