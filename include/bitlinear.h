@@ -192,7 +192,9 @@ bl_status bitlinear_quantize_acts_absmax(const void* x, int x_dtype, int M, int 
  *   xq        device, [M][K] int8, written.   scale  device, [M] fp32, written.
  *   rstd      device, [M] fp32, or NULL to skip: what bitlinear_rmsnorm_backward needs.
  * K <= 32768, else BL_ERR_UNSUPPORTED_SHAPE. Inf/NaN in x, residual or weight, or a row whose
- * sum of squares or largest |p| passes fp32, sets BL_ERR_NONFINITE in the status word. */
+ * sum of squares, largest |p| or largest normalised value passes fp32, sets BL_ERR_NONFINITE in
+ * the status word. The order in which a row's squares are added depends on M (rstd and scale can
+ * differ in their last places between batches; h and the codes do not). */
 bl_status bitlinear_rmsnorm_quantize(const void* x, const void* residual, int x_dtype,
                                      const void* weight, int w_dtype, float eps, int M, int K,
                                      void* h, void* normed, int8_t* xq, float* scale, float* rstd,

@@ -179,9 +179,10 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_quant_kernel(
       __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(K)), eps)));
   const float f = (m > 0.0f) ? __fdiv_rn(127.0f, m) : 0.0f;
   if (threadIdx.x == 0) {
-    // NaN or infinite: x or the residual by either, the gain by m
-    if (!(ss <= kFloatMax) || !(m <= kFloatMax)) record_status(kStatusNonfinite);
-    scale[t] = (m > 0.0f) ? __fdiv_rn(__fmul_rn(m, rstd), 127.0f) : 0.0f;
+    // NaN or infinite: x or the residual in either, the gain and the normalised row in top
+    const float top = __fmul_rn(m, rstd);
+    if (!(ss <= kFloatMax) || !(top <= kFloatMax)) record_status(kStatusNonfinite);
+    scale[t] = (m > 0.0f) ? __fdiv_rn(top, 127.0f) : 0.0f;
     if (rstd_out) rstd_out[t] = rstd;
   }
   int8_t* qrow = xq + static_cast<size_t>(t) * K;

@@ -267,3 +267,43 @@ def test_norm_statistics_of_squares_lost_one_by_one(K, dtype, every):
     rs = 1.0 / (x.double().square().mean(-1) + 1e-10).sqrt()
     assert ((rstd.cpu().double() - rs).abs() <= 28 * U * rs).all()
     assert ((scale.cpu().double() - rs / 127).abs() <= 30 * U * rs / 127).all()
+
+
+@pytest.mark.gpu
+def test_norm_reports_rows_whose_normalised_values_pass_fp32():
+    """One value in a row of 64 is 8 after the norm; a gain of 3e38 is finite, and so is p."""
+    x = torch.zeros((2, 64))
+    x[1, 3] = 1.0
+    w = torch.full((64,), 4e37)
+    bl.rmsnorm_quantize(x.cuda(), w.cuda(), eps=1e-12)
+    assert bl.get_device_status() == 0
+    w[3] = 3e38
+    bl.rmsnorm_quantize(x.cuda(), w.cuda(), eps=1e-12)
+    assert bl.get_device_status() == 6
+
+
+@pytest.mark.gpu
+def test_rows_beyond_4_gb():
+    """fp32 rows that begin past 2^32 bytes, forward and backward, against the same rows alone."""
+    K = 16384
+    M = (1 << 31) // K - 1  # the largest batch of these rows
+    last = torch.randn((3, K), generator=syn.gen(1)).cuda()
+    w = (1.0 + 0.2 * torch.randn(K, generator=syn.gen(2))).cuda()
+    x = torch.zeros((M, K), device="cuda")
+    x[-3:] = last
+    xq, scale, h, rstd = bl.rmsnorm_quantize(x, w, x, h=x)  # x + x, in place
+    xq1, scale1, h1, rstd1 = bl.rmsnorm_quantize(last, w, last)
+    assert torch.equal(xq[-3:], xq1) and torch.equal(h[-3:], h1) and (xq[:-3] == 0).all()
+    assert ((rstd[-3:] - rstd1).abs() <= 2 * 28 * U * rstd1).all()
+    assert ((scale[-3:] - scale1).abs() <= 2 * 30 * U * scale1).all()
+    del xq
+    g = torch.zeros((M, K), device="cuda")
+    g[-3:] = last.flip(1)
+    g1, rs = g[-3:].clone(), rstd.clone()
+    rs[-3:] = rstd1
+    gx, gw = bl.rmsnorm_backward(g, h, w, rs)
+    gx1, gw1 = bl.rmsnorm_backward(g1, h1, w, rstd1)
+    assert torch.equal(gx[-3:], gx1) and (gx[:-3] == 0).all()
+    mag = (g1.double() * h1.double() * rstd1.double()[:, None]).abs().sum(0)
+    assert ((gw - gw1).abs() <= 2 * 7 * U * mag).all()
+    assert bl.get_device_status() == 0
