@@ -296,7 +296,7 @@ def _random_tokens(M, E, D, seed):
     g = torch.Generator(device="cuda").manual_seed(seed)
     x = torch.randn((M, D), generator=g, device="cuda")
     x[:, :E] = torch.rand((M, E), generator=g, device="cuda").argsort(-1) / 32.0
-    return x.bfloat16()
+    return x.bfloat16() if E <= 256 else x  # more 32nds than bf16 holds
 
 
 def _trits64(packed):
@@ -360,6 +360,8 @@ def _reference_by_expert(x, layer, act, renorm):
     # up / down; 16 columns, gate and up / down
     (64, 128, 512, 1536, 8, "silu"), (64, 128, 4096, 64, 8, "silu"),
     (64, 8, 192, 8640, 2, "silu"), (64, 8, 16384, 64, 2, "relu2"),
+    # every limit: pairs, experts and choices; both widths
+    (64, 512, 512, 64, 16, "silu"), (64, 1, 16384, 16384, 1, "silu"),
 ])
 def test_moe_of_wide_rows_and_long_stretches(M, E, D, F, top_k, act):
     layer = _random_layer(E, D, F, seed=D + F, top_k=top_k, activation=act)

@@ -267,3 +267,37 @@ def test_gradients_within_the_bound_of_their_parts(M, N, K):
                              (gw, G.double().T @ xt, G.double().abs().T @ xt.abs(), M)):
         err = (got.cpu().double() - ref).abs()
         assert (err <= _split_bound(n, mag) + 2.0 ** -23 * ref.abs()).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [3, 40])
+def test_two_projections_of_one_row_on_two_streams_captured(M):
+    """Kernels that may start before the one ahead of them has ended, behind a fork and before a join:
+    the next norm adds what both streams left. As called, and from a graph."""
+    N, K = 512, 512
+    gain = torch.ones(K).cuda()
+    x, r = syn.activations(M, K, 1).cuda(), syn.activations(M, K, 2).cuda()
+    weights = [bl.quantize_weights(syn.weights(N, K, 0.02, seed=s).cuda()) for s in (3, 4)]
+    side = torch.cuda.Stream()
+
+    def step(other):
+        xq, scale, h, _ = bl.rmsnorm_quantize(x, gain, r)
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        a = bl.forward_quantized(xq, scale, *weights[0])
+        b = bl.forward_quantized(xq, scale, *weights[1], stream=side if other else None)
+        here.wait_stream(side)
+        return (a, b, *bl.rmsnorm_quantize(a, gain, b))
+
+    want = [t.clone() for t in step(False)]
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(step(True), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(True)
+    for _ in range(10):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert bl.get_device_status() == 0
