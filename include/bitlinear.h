@@ -37,6 +37,8 @@
  *  - Shapes: M, N >= 1; K >= 64 and K % 64 == 0; M*K, N*K and M*N below 2^31.
  *    Otherwise BL_ERR_UNSUPPORTED_SHAPE.
  *  - Alignment: every device pointer 16-byte aligned, else BL_ERR_MISALIGNED.
+ *  - Overlap: outputs and workspaces share no memory with other arguments, except where an
+ *    argument's description allows it.
  *  - Thread safety: calls on different streams may run concurrently; they share only the
  *    device status word.
  */

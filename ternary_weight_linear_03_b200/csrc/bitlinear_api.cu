@@ -1256,7 +1256,7 @@ struct NormPlan {
 // several blocks per SM overlap their loads, barriers and stores (4096 x 8192 bf16, 1 / 2 / 4
 // vectors: 55.3 / 42.9 / 46.8 us); four for short fp32 rows (1021 x 3200: 6.7 -> 5.6 us), and as
 // many as two blocks per SM need for rows that 1024 threads do not hold so (1170 x 28672 bf16:
-// 61.7 -> 53.9 us).
+// 61.7 -> 52.3 us).
 NormPlan norm_plan(int M, int K, bool bf16) {
   const int nv = K / 8;
   NormPlan p{};
